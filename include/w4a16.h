@@ -413,6 +413,54 @@ int awq_search_lookahead(const uint16_t* X, int B, int L, int hidden, int n_q, i
                          void* workspace, size_t* workspace_bytes, void* stream);
 
 /*
+ * MXFP4: linears whose weights (and, for mxfp4_a4_gemm, activations) are 4-bit
+ * microscaling floats.  ["OCP Microscaling Formats (MX) Specification v1.0", sections
+ * 5.2 and 6.3.]  Beside the conventions at the top of this file:
+ *   - 32 consecutive channels of a row form a block, so K must be a multiple of 32
+ *     (not of 128).  scales[n][b] (uint8, [N][K/32]) is the block's E8M0 byte: the
+ *     scale 2^(byte - 127); 255 is NaN.
+ *   - codes[n][i] (uint32, [N][K/8]) holds in nibble j the e2m1 code of channel
+ *     8 i + j: bit 3 the sign, bits 0-2 the magnitude 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   - The value of an element is its magnitude with its sign times its block's scale.
+ *   - A call with N == 0 (or M == 0) succeeds and enqueues nothing.
+ *
+ * mxfp4_quantize -- v = W diag(s) to MXFP4, weights and activations alike.  Per block,
+ *   with v = W[n][k] s[k] in fp32 (s == NULL: v = W[n][k]) and A = max |v|:
+ *     byte = max(floor(log2 A) - 2 + 127, 0)  (0 for A = 0 or subnormal A),
+ *     code = v / 2^(byte - 127) rounded to the nearest magnitude, ties to the even
+ *            code, saturating at 6; the sign of v is kept, also that of zero.
+ *   A block with an infinite or NaN v gets byte 255 and codes 0.  Bit-identical to
+ *   this definition for every input.
+ *   W [N][K] bf16.  s [K] fp32 or NULL.  codes [N][K/8], scales [N][K/32] out.
+ */
+int mxfp4_quantize(const uint16_t* W, int N, int K, const float* s, uint32_t* codes, uint8_t* scales,
+                   void* stream);
+
+/*
+ * mxfp4_dequantize -- the values of MXFP4 elements as bf16, W [N][K] out.  Exact, except
+ *   that magnitudes past bf16's range (scale bytes 253 and 254) become infinite;
+ *   elements of a block with byte 255 become NaN.
+ */
+int mxfp4_dequantize(const uint32_t* codes, const uint8_t* scales, int N, int K, uint16_t* W, void* stream);
+
+/*
+ * mxfp4_a16_gemm -- Y = X W_hat^T with 16-bit activations and MXFP4 weights, any M.
+ * mxfp4_a4_gemm  -- Y = X_hat W_hat^T with both operands MXFP4 (activations as
+ *   mxfp4_quantize writes them), any M, on the block-scaled matrix cores.
+ *   X [M][K] bf16; Xq [M][K/8] and xscales [M][K/32]; qweight [N][K/8] and scales
+ *   [N][K/32].  Y [M][N] bf16 out: exact products, fp32 accumulation in an order fixed
+ *   by (M, K, N), rounded to nearest even at the store.  A weight block with byte 255
+ *   makes its output channel NaN, an activation block with byte 255 its row;
+ *   mxfp4_a16_gemm takes weights as the bf16 values of mxfp4_dequantize.
+ *   W4_ERR_SHAPE (from the size query too) when K > 2,097,152.
+ *   Size query and workspace as in w4a16_gemv; the size depends only on (M, K, N).
+ */
+int mxfp4_a16_gemm(const uint16_t* X, int M, int K, int N, const uint32_t* qweight, const uint8_t* scales,
+                   uint16_t* Y, void* workspace, size_t* workspace_bytes, void* stream);
+int mxfp4_a4_gemm(const uint32_t* Xq, const uint8_t* xscales, int M, int K, int N, const uint32_t* qweight,
+                  const uint8_t* scales, uint16_t* Y, void* workspace, size_t* workspace_bytes, void* stream);
+
+/*
  * Measurement helpers (not part of the method): the yardsticks the kernels
  * above are measured against on the same device.
  *

@@ -22,10 +22,13 @@ __all__ = [
     "awq_grid_loss", "awq_search", "GROUP_SIZE", "GEMV_MAX_M", "gemv_launcher", "gemm_launcher",
     "w4a8_quantize_activations", "w4a8_gemv", "w4a8_gemv_launcher", "awq_clip_search", "block_forward",
     "block_forward_quantized", "awq_lookahead_loss", "awq_search_lookahead", "BLOCK_LINEARS", "probe_stream_read", "probe_empty",
+    "MX_BLOCK", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_a16_gemm", "mxfp4_a4_gemm", "mxfp4_a16_gemm_launcher",
+    "mxfp4_a4_gemm_launcher",
 ]
 
 GROUP_SIZE = 128
 GEMV_MAX_M = 16
+MX_BLOCK = 32
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
 
@@ -62,6 +65,10 @@ _SIGNATURES = {
     "awq_search_lookahead": ([_vp, _i, _i, _i, _i, _i, _i, _bp, _bp, _i, ctypes.POINTER(ctypes.c_double), _i,
                               ctypes.POINTER(ctypes.c_double), _i, _i, _i, ctypes.POINTER(ctypes.c_float),
                               ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int), _vp, _vp, _sz, _vp], _i),
+    "mxfp4_quantize": ([_vp, _i, _i, _vp, _vp, _vp, _vp], _i),
+    "mxfp4_dequantize": ([_vp, _vp, _i, _i, _vp, _vp], _i),
+    "mxfp4_a16_gemm": ([_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp], _i),
+    "mxfp4_a4_gemm": ([_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp], _i),
     "awq_search": ([_vp, _i, _i, _i, _vp, ctypes.POINTER(ctypes.c_double), _i,
                     ctypes.POINTER(ctypes.c_double), _i, _i, _i, ctypes.POINTER(ctypes.c_float),
                     ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int), _vp, _vp, _sz, _vp], _i),
@@ -566,6 +573,129 @@ def gemv_launcher(X, qweight, scales, qzeros, symmetric: bool, Y, workspace=None
 def gemm_launcher(X, qweight, scales, qzeros, symmetric: bool, Y, workspace=None):
     """As gemv_launcher, for the MFMA GEMM."""
     return _launcher("w4a16_gemm", X, qweight, scales, qzeros, symmetric, Y, workspace)
+
+
+def _mx_need(t, dtype, name, shape, device):
+    _need(t, dtype, name, len(shape))
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _mx_call(fn, args, device):
+    # kernels go to the current device: make it the tensors' own for the call
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(device)))
+
+
+def _mx_width(t, per, name):
+    """K of a matrix stored with `per` channels per element of its rows."""
+    K = t.shape[1] * per
+    if K == 0 or K % MX_BLOCK:
+        raise ValueError(f"{name}: K must be a positive multiple of {MX_BLOCK}, got {K}")
+    return K
+
+
+def mxfp4_quantize(W, s=None, codes=None, scales=None):
+    """Quantize W [N][K] bf16 (times diag(s)) to MXFP4, K a multiple of 32.
+
+    Returns (codes int32 [N][K/8], scales uint8 [N][K/32]); see include/w4a16.h."""
+    lib = load_library()
+    _need(W, torch.bfloat16, "W", 2)
+    dev = W.device
+    N, K = W.shape[0], _mx_width(W, 1, "W")
+    if s is not None:
+        _mx_need(s, torch.float32, "s", (K,), dev)
+    if codes is None:
+        codes = torch.empty((N, K // 8), dtype=torch.int32, device=dev)
+    else:
+        _mx_need(codes, torch.int32, "codes", (N, K // 8), dev)
+    if scales is None:
+        scales = torch.empty((N, K // MX_BLOCK), dtype=torch.uint8, device=dev)
+    else:
+        _mx_need(scales, torch.uint8, "scales", (N, K // MX_BLOCK), dev)
+    _mx_call(lib.mxfp4_quantize, (_ptr(W), N, K, _ptr(s), _ptr(codes), _ptr(scales)), dev)
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, W=None):
+    """The values of MXFP4 elements: W [N][K] bf16 from codes int32 [N][K/8], scales uint8 [N][K/32]."""
+    lib = load_library()
+    _need(codes, torch.int32, "codes", 2)
+    dev = codes.device
+    N, K = codes.shape[0], _mx_width(codes, 8, "codes")
+    _mx_need(scales, torch.uint8, "scales", (N, K // MX_BLOCK), dev)
+    if W is None:
+        W = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+    else:
+        _mx_need(W, torch.bfloat16, "W", (N, K), dev)
+    _mx_call(lib.mxfp4_dequantize, (_ptr(codes), _ptr(scales), N, K, _ptr(W)), dev)
+    return W
+
+
+def _mx_gemm_launcher(cname, acts, qweight, scales, Y, workspace):
+    """Check the operands of a product and bind its call; acts is (X,) or (Xq, xscales)."""
+    lib = load_library()
+    if len(acts) == 1:
+        _need(acts[0], torch.bfloat16, "X", 2)
+        dev, M, K = acts[0].device, acts[0].shape[0], _mx_width(acts[0], 1, "X")
+    else:
+        _need(acts[0], torch.int32, "Xq", 2)
+        dev, M, K = acts[0].device, acts[0].shape[0], _mx_width(acts[0], 8, "Xq")
+        _mx_need(acts[1], torch.uint8, "xscales", (M, K // MX_BLOCK), dev)
+    _need(qweight, torch.int32, "qweight", 2)
+    N = qweight.shape[0]
+    _mx_need(qweight, torch.int32, "qweight", (N, K // 8), dev)
+    _mx_need(scales, torch.uint8, "scales", (N, K // MX_BLOCK), dev)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _mx_need(Y, torch.bfloat16, "Y", (M, N), dev)
+    if workspace is not None:
+        _mx_need(workspace, torch.uint8, "workspace", (workspace.numel(),), dev)
+    fn = getattr(lib, cname)
+
+    def q(sz):
+        return fn(*(None for _ in acts), M, K, N, None, None, None, None, sz, None)
+
+    ws, wsb = _workspace(q, dev, workspace)
+    args = (*map(_ptr, acts), M, K, N, _ptr(qweight), _ptr(scales), _ptr(Y), _ptr(ws),
+            None if wsb is None else ctypes.byref(wsb))
+
+    def launch():
+        _mx_call(fn, args, dev)
+
+    launch.tensors = (*acts, qweight, scales, Y, ws)     # kept alive while the launcher is
+    launch.workspace_size = wsb
+    return launch, Y
+
+
+def mxfp4_a16_gemm(X, qweight, scales, Y=None, workspace=None):
+    """Y [M][N] bf16 = X [M][K] bf16 times the MXFP4 weight (mxfp4_quantize), transposed; any M."""
+    launch, Y = _mx_gemm_launcher("mxfp4_a16_gemm", (X,), qweight, scales, Y, workspace)
+    launch()
+    return Y
+
+
+def mxfp4_a4_gemm(Xq, xscales, qweight, scales, Y=None, workspace=None):
+    """Y [M][N] bf16 = MXFP4 activations (mxfp4_quantize) times the MXFP4 weight, transposed; any M."""
+    launch, Y = _mx_gemm_launcher("mxfp4_a4_gemm", (Xq, xscales), qweight, scales, Y, workspace)
+    launch()
+    return Y
+
+
+def mxfp4_a16_gemm_launcher(X, qweight, scales, Y, workspace=None):
+    """As gemv_launcher, for mxfp4_a16_gemm."""
+    return _mx_gemm_launcher("mxfp4_a16_gemm", (X,), qweight, scales, Y, workspace)[0]
+
+
+def mxfp4_a4_gemm_launcher(Xq, xscales, qweight, scales, Y, workspace=None):
+    """As gemv_launcher, for mxfp4_a4_gemm."""
+    return _mx_gemm_launcher("mxfp4_a4_gemm", (Xq, xscales), qweight, scales, Y, workspace)[0]
 
 
 def probe_stream_read(buf, unroll: int = 4, nontemporal: bool = False, blocks: int = 0, sink=None):

@@ -135,6 +135,27 @@ int launch_bf16_glu(const uint16_t* X, int M, int K, int N, const uint16_t* Wg, 
 int launch_reference_gemm(const uint16_t* X, int M, int K, int N, const uint16_t* W, uint16_t* Y,
                           hipStream_t stream);
 
+// ---------------------------------------------------------------- MXFP4
+int launch_mxfp4_quantize(const uint16_t* W, int N, int K, const float* s, uint32_t* codes, uint8_t* scales,
+                          hipStream_t stream);
+int launch_mxfp4_dequantize(const uint32_t* codes, const uint8_t* scales, int N, int K, uint16_t* W,
+                            hipStream_t stream);
+struct MxGemmArgs {
+  int act_bits;              // 16: X; 4: Xq and xscales
+  const uint16_t* X;         // [M][K] bf16
+  const uint32_t* Xq;        // [M][K/8] codes
+  const uint8_t* xscales;    // [M][K/32]
+  int M, K, N;
+  const uint32_t* qweight;   // [N][K/8] codes
+  const uint8_t* scales;     // [N][K/32]
+  uint16_t* Y;               // [M][N] bf16
+  void* workspace;
+};
+// A function of its arguments alone, so the size query (made without a device) and the
+// launch agree.
+size_t mxfp4_gemm_workspace_bytes(int act_bits, int M, int K, int N);
+int launch_mxfp4_gemm(const MxGemmArgs& g, hipStream_t stream);
+
 // m_k = mean_t |X[t][k]| in fp64, fixed summation order.
 // m must hold (1 + ceil(T / 64)) * K doubles: m[0..K) is the result, the rest
 // per-chunk partial sums.
