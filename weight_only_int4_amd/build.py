@@ -31,11 +31,16 @@ HIPCC_FLAGS = [
     "-Wall",
     "-Wno-unused-function",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # keep MFMA accumulators in ordinary VGPRs: the int4 GEMM folds them with VALU
-    # FMAs every group, and accumulator-register copies would double its VALU work
-    "-mllvm", "-amdgpu-mfma-vgpr-form=1",
     "-I", os.path.join(ROOT, "include"),
 ]
+
+
+# keep MFMA accumulators in ordinary VGPRs: the int4 GEMM folds them with VALU
+# FMAs every group, and accumulator-register copies would double its VALU work
+VGPR_ACC_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+# kernels that never touch their accumulators between MFMAs, and need all 512 registers
+# of one wave per SIMD
+ACC_REGISTER_SOURCES = {"mxfp4_gemm.hip"}
 
 
 # the library links nothing beyond the HIP runtime
@@ -55,7 +60,8 @@ def sources():
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    cmd = [hipcc(), *HIPCC_FLAGS, "-c", src, "-o", obj]
+    form = [] if os.path.basename(src) in ACC_REGISTER_SOURCES else VGPR_ACC_FLAGS
+    cmd = [hipcc(), *HIPCC_FLAGS, *form, "-c", src, "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{res.stdout}\n{res.stderr}")

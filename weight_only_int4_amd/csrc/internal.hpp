@@ -151,8 +151,22 @@ struct MxGemmArgs {
   uint16_t* Y;               // [M][N] bf16
   void* workspace;
 };
-// A function of its arguments alone, so the size query (made without a device) and the
-// launch agree.
+// Plans are functions of their arguments alone, so the size query (made without a device)
+// and the launch agree.  The stream form (mxfp4_stream.hip) reads both operands into
+// registers, the tiled form (mxfp4_gemm.hip) goes through LDS.
+struct MxStreamPlan {
+  int slices, rows, cols, waves, splits;   // K slices per tile, row tiles, channel tiles, waves, split of K
+};
+struct MxTilePlan {
+  int tile, splits, stages;                // tile shape, split of K, 128-channel stages of a split
+  double us;                               // estimated time
+};
+MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N);
+MxTilePlan plan_mx_tile(int act_bits, int M, int K, int N);
+bool mxfp4_use_tile(int act_bits, int M, int K, int N);
+size_t mx_tile_workspace_bytes(const MxTilePlan& p, int act_bits, int M, int K, int N);
+int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t stream);
+int launch_mx_tile(const MxTilePlan& p, const MxGemmArgs& g, hipStream_t stream);
 size_t mxfp4_gemm_workspace_bytes(int act_bits, int M, int K, int N);
 int launch_mxfp4_gemm(const MxGemmArgs& g, hipStream_t stream);
 

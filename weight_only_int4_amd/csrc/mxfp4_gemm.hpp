@@ -1,0 +1,504 @@
+// Tiled products with MXFP4 weights, Y = X W_hat^T, for row counts at which the
+// matrix cores are the bound: MXFP4 activations (mx_tile_a4_kernel) or bf16 ones
+// (mx_tile_a16_kernel).
+//
+// A workgroup of eight waves owns BM rows x BN channels, WM x WN waves each with FM x FN
+// tiles of 16 x 16.  K goes in stages of 128 channels that travel from global memory
+// straight into LDS (global_load_lds, no registers), S slots deep.  The weights are the
+// matrix instruction's row operand, so a lane ends with four consecutive channels of
+// one output row.
+//
+// Two waves share a SIMD (wave w and w + 4), and they work in opposite phases: while
+// one reads its fragments from LDS, the other runs its matrix instructions, and a
+// barrier swaps them.  In one phase both would queue at the LDS first and at the
+// matrix cores afterwards (measured: LDS and matrix time then add up).
+//
+// LDS layout: a row of codes is 64 bytes of a stage, chunk q (16 bytes) one MX block;
+// position p of row r holds chunk p ^ ((r >> 2) & 3).  A row of bf16 activations is 256
+// bytes, position p holding chunk p ^ (r & 15).  A 16-lane pass of fragment reads (16
+// rows, one chunk) then covers all 64 banks once.
+//
+// Scale bytes come 16 at a time (four stages of a row, one 16-byte LDS read): an LDS
+// read of one byte per lane costs nearly as much as one of 16 (2.9 against 3.5 ns per
+// wave).  Lane (r, q) keeps byte q of each stage's dword, packed into one register.
+//
+// Rows past M or N re-read the last row (their outputs are not stored).  When K is not a
+// multiple of 128, copies of the last stage clamp to the blocks that exist and the lanes
+// of the missing ones zero their operands.  Rows of the scale arrays are multiples of
+// four bytes, at least 16 long (the caller pads them with zeros otherwise).
+#pragma once
+
+#include "gemm_core.hpp"
+#include "mxfp4.hpp"
+
+namespace w4 {
+
+struct MxTileArgs {
+  const void* X;            // [M][K] bf16, or [M][K/8] codes
+  const uint8_t* xs;        // [M][ss] scale bytes (MXFP4 activations)
+  const uint32_t* qweight;  // [N][K/8]
+  const uint8_t* ws;        // [N][ss]
+  int ss;                   // bytes of a scale row: a multiple of 4, at least 16
+  int M, K, N;
+  int stages_per_split;     // stages of blockIdx.y: [y, y + 1) * stages_per_split, a multiple of 4
+  uint16_t* Y;              // [M][N], or
+  float* partial;           // [splits][M][N] when not NULL
+};
+
+constexpr int kMxWaves = 8;
+
+__device__ __forceinline__ void mx_phase_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  lds_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Byte q of each of four dwords, packed in order; sel = q | (q + 4) << 8 selects byte q
+// of the second and of the first source of v_perm_b32.
+__device__ __forceinline__ uint32_t pack_bytes(u32x4 d, uint32_t sel) {
+  const uint32_t lo = __builtin_amdgcn_perm(d[1], d[0], sel), hi = __builtin_amdgcn_perm(d[3], d[2], sel);
+  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+
+// The tile's outputs: lane (c, q) of tile (i, j) holds row c, channels 4 q .. 4 q + 3, so
+// a store straight from there writes 32-byte pieces.  bf16 rows go through `stage`, this
+// wave's own kMxStage<FN> bytes of LDS (16 rows, padded by 16 bytes against bank
+// conflicts), and leave in 16-byte pieces of whole rows.
+template <int FN>
+constexpr int kMxStage = 16 * (FN * 32 + 16);
+
+// Rows of P-element pieces; P divides N, so pieces are whole and aligned.
+template <int FM, int FN, int P>
+__device__ __forceinline__ void mx_store_rows(const MxTileArgs& a, const f32x4 (&acc)[FM][FN], int m1, int n1,
+                                              unsigned char* stage) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  typedef uint16_t piece __attribute__((ext_vector_type(P)));
+  constexpr int kRow = FN * 32 + 16, kPieces = FN * 16 / P;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const bf16x4 b = {(__bf16)acc[i][j][0], (__bf16)acc[i][j][1], (__bf16)acc[i][j][2], (__bf16)acc[i][j][3]};
+      *reinterpret_cast<bf16x4*>(stage + r * kRow + j * 32 + q * 8) = b;
+    }
+    __builtin_amdgcn_wave_barrier();            // LDS operations of one wave complete in order
+#pragma unroll 4
+    for (int p = lane; p < 16 * kPieces; p += 64) {
+      const int row = p / kPieces, c = p % kPieces;
+      const int m = m1 + 16 * i + row, n = n1 + P * c;
+      if (m < a.M && n < a.N)
+        *reinterpret_cast<piece*>(a.Y + (size_t)m * a.N + n) = *reinterpret_cast<const piece*>(stage + row * kRow + c * (2 * P));
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <int FM, int FN>
+__device__ __forceinline__ void mx_store_tile(const MxTileArgs& a, const f32x4 (&acc)[FM][FN], int m1, int n1,
+                                              unsigned char* stage) {
+  if (!a.partial) {
+    if ((a.N & 7) == 0) mx_store_rows<FM, FN, 8>(a, acc, m1, n1, stage);
+    else if ((a.N & 1) == 0) mx_store_rows<FM, FN, 2>(a, acc, m1, n1, stage);
+    else mx_store_rows<FM, FN, 1>(a, acc, m1, n1, stage);
+    return;
+  }
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  float* part = a.partial + (size_t)blockIdx.y * a.M * a.N;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int m = m1 + 16 * i + r;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int n = n1 + 16 * j + 4 * q;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < a.N) part[(size_t)m * a.N + n + e] = acc[i][j][e];
+    }
+  }
+}
+
+// MXFP4 activations.  Four waves (2 x 2), one per SIMD, BM / 2 rows x BN / 2 channels each.
+template <int BM, int BN>
+__global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
+  constexpr int W = 4;                          // waves
+  static_assert(BM % 64 == 0 && BN % 64 == 0, "copies and scale copies cover 64 rows");
+  constexpr int FM = BM / 32, FN = BN / 32, F = FM + FN, T = FM * FN;
+  constexpr int kRows = BM + BN;                // activation rows, then channels
+  constexpr int kSlot = kRows * 128, kScales = 2 * kSlot, kGroup4 = kRows * 16;
+  constexpr int C = kRows / 8 / W;              // 1 KB copies (8 rows) per wave and pair of stages
+  constexpr int kSUnits = kRows / 64;           // 1 KB copies per four stages of scales
+  constexpr int CS = (kSUnits + W - 1) / W;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * kSlot + 2 * kGroup4];
+  constexpr int kEvery = T / C;                 // matrix instructions per copy
+  static_assert(kEvery >= 1 && C * kEvery < 2 * T, "a pair's copies fit two steps");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int r = lane & 15, q = lane >> 4;
+  int tm, tn;
+  tile_coords(blockIdx.x, (a.M + BM - 1) / BM, (a.N + BN - 1) / BN, tm, tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int KB = a.K / kMxBlock, KT = (KB + 3) / 4;
+  const int kt0 = blockIdx.y * a.stages_per_split, kt1 = min(KT, kt0 + a.stages_per_split);
+  const int n_stages = kt1 - kt0;
+  const int rem = KB & 3;                       // blocks of the last stage, 0: all four
+  const uint32_t smem_base = (uint32_t)(uintptr_t)smem;
+  const uint32_t rowb = (uint32_t)a.K / 2u;
+  const unsigned char* xb = static_cast<const unsigned char*>(a.X) + (size_t)m0 * rowb;
+  const unsigned char* wb = reinterpret_cast<const unsigned char*>(a.qweight) + (size_t)n0 * rowb;
+  const unsigned char* xsb = a.xs + (size_t)m0 * a.ss;
+  const unsigned char* wsb = a.ws + (size_t)n0 * a.ss;
+  const int mlast = a.M - 1 - m0, nlast = a.N - 1 - n0;
+
+  // Stages travel in pairs, so that a row's piece is a whole 128-byte line (64-byte pieces
+  // cost the L1 as much: 505 against 254 ns per 32 KB and CU).  Copy u of this wave is
+  // unit wave + 4 u: rows 8 (wave + 4 u) + lane / 8, position lane % 8 holding chunk
+  // (lane % 8) ^ ((row >> 1) & 7), the same for every u.
+  uint32_t off[C], soff[CS];
+  auto is_x = [](int u) { return u < BM / 8 / W; };            // compile-time: activations first
+#pragma unroll
+  for (int u = 0; u < C; ++u) {
+    const int row = (wave + W * u) * 8 + (lane >> 3) - (is_x(u) ? 0 : BM);
+    off[u] = (uint32_t)min(row, is_x(u) ? mlast : nlast) * rowb;
+  }
+#pragma unroll
+  for (int u = 0; u < CS; ++u) {
+    const int unit = min(wave + W * u, kSUnits - 1);
+    const bool isx = unit < BM / 64;
+    const int row = unit * 64 + lane - (isx ? 0 : BM);
+    soff[u] = (uint32_t)min(row, isx ? mlast : nlast) * (uint32_t)a.ss;
+  }
+  const int chunk = (lane & 7) ^ (((wave * 8 + (lane >> 3)) >> 1) & 7);
+  // Copies of pair p of stages counted from kt0, into slot p % 2; past the end the last
+  // pair is copied again, into a slot that nothing reads any more.
+  struct Src {
+    const unsigned char *x, *w;
+    uint32_t c;
+  };
+  auto source = [&](int pair) {
+    const int kt = kt0 + 2 * min(pair, (n_stages - 1) >> 1);
+    return Src{xb + (size_t)kt * 64, wb + (size_t)kt * 64, 16u * (uint32_t)min(chunk, min(8, KB - 4 * kt) - 1)};
+  };
+  auto copy = [&](const Src& s, int slot, int u) {
+    lds_copy16(off[u] + s.c, is_x(u) ? s.x : s.w, smem_base + (uint32_t)(slot * kSlot + (wave + W * u) * 1024));
+  };
+  // A group's first stage, moved back where the row ends before the group does.
+  auto group_start = [&](int group) { return max(0, min(kt0 + 4 * group, KT - 4)); };
+  auto copy_scales = [&](int group) {
+    const int ks = group_start(group);
+#pragma unroll
+    for (int u = 0; u < CS; ++u) {
+      const int unit = min(wave + W * u, kSUnits - 1);
+      lds_copy16(soff[u], (unit < BM / 64 ? xsb : wsb) + (size_t)ks * 4,
+                 smem_base + kScales + (uint32_t)(group & 1) * kGroup4 + unit * 1024);
+    }
+  };
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  // fragment e: channels for e < FN, activation rows after; row 16 e' + r of this wave's
+  // part ((row >> 1) & 7 does not depend on e'), chunk 4 h + q of the pair's stage h
+  const uint32_t swz = (uint32_t)((q ^ ((r >> 1) & 7)) * 16);
+  const uint32_t xfrag = (uint32_t)((wm * FM * 16 + r) * 128) + swz;
+  const uint32_t wfrag = (uint32_t)((BM + wn * FN * 16 + r) * 128) + swz;
+  const uint32_t xsrow = (uint32_t)(kScales + (wm * FM * 16 + r) * 16);
+  const uint32_t wsrow = (uint32_t)(kScales + (BM + wn * FN * 16 + r) * 16);
+  const uint32_t sel = (uint32_t)(q | ((q + 4) << 8)) | 0x0C0C0000u;
+
+  u32x4 f[2][F];                                // fragments of this stage and the next
+  uint32_t sc[F], scn[F];                       // packed scale bytes of four stages, and the next four
+  auto read = [&](int buf, int j4, int e) {     // stage j4 of four: slot j4 / 2, half j4 % 2
+    const uint32_t o = e < FN ? (wfrag ^ (uint32_t)(64 * (j4 & 1))) + e * 2048
+                              : (xfrag ^ (uint32_t)(64 * (j4 & 1))) + (e - FN) * 2048;
+    f[buf][e] = *reinterpret_cast<const u32x4*>(smem + (j4 >> 1) * kSlot + o);
+  };
+  auto read_scales = [&](int group, int e) {
+    const uint32_t o = e < FN ? wsrow + e * 256 : xsrow + (e - FN) * 256;
+    return *reinterpret_cast<const u32x4*>(smem + (uint32_t)(group & 1) * kGroup4 + o);
+  };
+  auto shift_of = [&](int group) { return 8 * min(3, kt0 + 4 * group - group_start(group)); };
+
+  // One stage; J = stage % 4 selects its slot, half and scale byte.  The stage's fragments are in
+  // registers when it starts, and between the matrix instructions the wave reads the next
+  // stage's (scales: the next four stages').  So a pair's slot is free when its second stage
+  // starts: that step waits for the next pair, meets the other waves and refills the
+  // slot, copies first, two stages before they are needed.
+  auto step = [&](auto jc, int s) {
+    constexpr int J = decltype(jc)::value;
+    constexpr int cur = J & 1, nxt = cur ^ 1;
+    const int stage = s + J;
+    if constexpr (cur == 1) {
+      wait_vmcnt<0>();
+      mx_phase_barrier();
+    }
+    const Src src = source((stage >> 1) + (cur == 1 ? 2 : 1));
+    if (rem != 0 && kt0 + stage == KT - 1 && q >= rem) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) f[cur][j] = u32x4{0, 0, 0, 0};
+    }
+    // Between the matrix instructions: a copy every kEvery of them, from the second step of
+    // a pair on into the first step of the next (in a burst they would fill the memory
+    // pipeline and hold back the wave's matrix instructions); reads one each.
+    constexpr int kLag = 3;                     // a scale read is packed three operations later
+    constexpr int kCopies = C + 1;              // the pair's, and every other pair scales
+    constexpr int kReads = F + (J == 3 ? F + kLag : 0);
+    constexpr int kPer = (kReads + T - 1) / T;  // more than one where the tile is small
+    u32x4 raw[F];
+    const int group = (stage + 1) >> 2, shift = J == 3 ? shift_of(group) : 0;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const int tc = cur == 1 ? t : T + t;      // matrix instructions since the pair's slot was free
+      if (tc % kEvery == 0 && tc / kEvery < kCopies) {
+        const int u = tc / kEvery;
+        constexpr int slot = cur == 1 ? J >> 1 : (J >> 1) ^ 1;
+        if (u == 0) { if constexpr (J == 1 || J == 2) copy_scales((stage + 3) >> 2); }
+        else copy(src, slot, u - 1);
+      }
+#pragma unroll
+      for (int o = t * kPer; o < (t + 1) * kPer; ++o) {
+        if (o < F) {
+          read(nxt, (J + 1) % 4, o);
+        } else if (o < kReads) {
+          const int e = o - F;
+          if (e >= kLag) scn[e - kLag] = pack_bytes(raw[e - kLag], sel) >> shift;
+          if (e < F) raw[e] = read_scales(group, e);
+        }
+      }
+      const int i = t / FN, j = t % FN;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(f[cur][j]), mx_operand(f[cur][FN + i]),
+                                                                  acc[i][j], 4, 4, J, (int)sc[j], J, (int)sc[FN + i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (J == 3) {
+#pragma unroll
+      for (int e = 0; e < F; ++e) sc[e] = scn[e];
+    }
+  };
+
+  constexpr int kEarly = (T - 1) / kEvery < C ? (T - 1) / kEvery : C;
+  copy_scales(0);
+  {
+    const Src p0 = source(0), p1 = source(1);
+#pragma unroll
+    for (int u = 0; u < C; ++u) copy(p0, 0, u);
+    // of pair 1 the copies that a second step would have issued; the first step issues the rest
+#pragma unroll
+    for (int u = 0; u < kEarly; ++u) copy(p1, 1, u);
+  }
+  wait_vmcnt<kEarly>();
+  mx_phase_barrier();
+#pragma unroll
+  for (int e = 0; e < F; ++e) {
+    read(0, 0, e);
+    sc[e] = pack_bytes(read_scales(0, e), sel) >> shift_of(0);
+  }
+  for (int s = 0; s < n_stages; s += 4) {
+    step(std::integral_constant<int, 0>{}, s);
+    if (s + 1 < n_stages) step(std::integral_constant<int, 1>{}, s);
+    if (s + 2 < n_stages) step(std::integral_constant<int, 2>{}, s);
+    if (s + 3 < n_stages) step(std::integral_constant<int, 3>{}, s);
+  }
+  wait_vmcnt<0>();
+  lds_barrier();                                // no copy and no read of the slots is left
+  mx_store_tile<FM, FN>(a, acc, m0 + wm * FM * 16, n0 + wn * FN * 16, smem + wave * kMxStage<FN>);
+}
+
+// bf16 activations.  Four waves (2 x 2), one per SIMD, BM / 2 rows x BN / 2 channels each.
+// A stage of 128 channels is four steps of 32: step v multiplies word v of every MX block
+// (channels 8 v .. 8 v + 7 of it), expanded to bf16, with chunk 4 q + v of the
+// activation rows.  Two slots; a slot is free when the fragments of its last step are read.
+template <int BM, int BN>
+__global__ __launch_bounds__(256, 1) void mx_tile_a16_kernel(MxTileArgs a) {
+  constexpr int W = 4;                          // waves
+  static_assert(BM % 64 == 0 && BN % 64 == 0, "copies and scale copies cover 64 rows");
+  constexpr int FM = BM / 32, FN = BN / 32, T = FM * FN;
+  constexpr int kX = 0, kW = BM * 256, kSlot = kW + BN * 64;
+  constexpr int kScales = 2 * kSlot, kGroup4 = BN * 16;
+  constexpr int CX = BM / 4 / W, CW = BN / 16 / W, C = CX + CW;   // 1 KB copies per wave and stage
+  constexpr int kSUnits = BN / 64, CS = (kSUnits + W - 1) / W;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * kSlot + 2 * kGroup4];
+  constexpr int kEvery = 2 * T / C;             // matrix instructions per copy: over two of the four steps
+  static_assert(kEvery >= 1 && C * kEvery < 4 * T, "a stage's copies fit its steps");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int r = lane & 15, q = lane >> 4;
+  int tm, tn;
+  tile_coords(blockIdx.x, (a.M + BM - 1) / BM, (a.N + BN - 1) / BN, tm, tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int KB = a.K / kMxBlock, KT = (KB + 3) / 4;
+  const int kt0 = blockIdx.y * a.stages_per_split, kt1 = min(KT, kt0 + a.stages_per_split);
+  const int n_stages = kt1 - kt0;
+  const int rem = KB & 3;                       // blocks of the last stage, 0: all four
+  const uint32_t smem_base = (uint32_t)(uintptr_t)smem;
+  const uint32_t xrowb = (uint32_t)a.K * 2u, wrowb = (uint32_t)a.K / 2u;
+  const unsigned char* xb = static_cast<const unsigned char*>(a.X) + (size_t)m0 * xrowb;
+  const unsigned char* wb = reinterpret_cast<const unsigned char*>(a.qweight) + (size_t)n0 * wrowb;
+  const unsigned char* wsb = a.ws + (size_t)n0 * a.ss;
+  const int mlast = a.M - 1 - m0, nlast = a.N - 1 - n0;
+
+  // Activation copy u: rows 4 (wave + 4 u) + lane / 16, position lane % 16 holding chunk
+  // (lane % 16) ^ (row & 15), and row & 15 is the same for every u.  Code copy u: rows
+  // 16 (wave + 4 u) + lane / 4, position lane % 4 holding chunk (lane % 4) ^ ((row >> 2) & 3).
+  uint32_t xoff[CX], woff[CW], soff[CS];
+#pragma unroll
+  for (int u = 0; u < CX; ++u) xoff[u] = (uint32_t)min((wave + W * u) * 4 + (lane >> 4), mlast) * xrowb;
+#pragma unroll
+  for (int u = 0; u < CW; ++u) woff[u] = (uint32_t)min((wave + W * u) * 16 + (lane >> 2), nlast) * wrowb;
+#pragma unroll
+  for (int u = 0; u < CS; ++u) soff[u] = (uint32_t)min(min(wave + W * u, kSUnits - 1) * 64 + lane, nlast) * (uint32_t)a.ss;
+  const int xchunk = (lane & 15) ^ ((wave * 4 + (lane >> 4)) & 15), wchunk = (lane & 3) ^ ((lane >> 4) & 3);
+  // Copies of a stage counted from kt0 into slot stage % 2; past the end the last stage is
+  // copied again, into a slot that nothing reads any more.
+  struct Src {
+    const unsigned char *x, *w;
+    uint32_t cx, cw;
+  };
+  auto source = [&](int stage) {
+    const int kt = kt0 + min(stage, n_stages - 1);
+    const int blocks = rem != 0 && kt == KT - 1 ? rem : 4;
+    return Src{xb + (size_t)kt * 256, wb + (size_t)kt * 64, 16u * (uint32_t)min(xchunk, 4 * blocks - 1),
+               16u * (uint32_t)min(wchunk, blocks - 1)};
+  };
+  auto copy = [&](const Src& s, uint32_t slot, int u) {
+    if (u < CX) lds_copy16(xoff[u] + s.cx, s.x, smem_base + slot + (uint32_t)(kX + (wave + W * u) * 1024));
+    else lds_copy16(woff[u - CX] + s.cw, s.w, smem_base + slot + (uint32_t)(kW + (wave + W * (u - CX)) * 1024));
+  };
+  // A group's first stage, moved back where the row ends before the group does.
+  auto group_start = [&](int group) { return max(0, min(kt0 + 4 * group, KT - 4)); };
+  auto copy_scales = [&](int group) {
+    const int ks = group_start(group);
+#pragma unroll
+    for (int u = 0; u < CS; ++u)
+      lds_copy16(soff[u], wsb + (size_t)ks * 4,
+                 smem_base + kScales + (uint32_t)(group & 1) * kGroup4 + min(wave + W * u, kSUnits - 1) * 1024);
+  };
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint32_t xrow = (uint32_t)(kX + (wm * FM * 16 + r) * 256);
+  const uint32_t wfrag = (uint32_t)(kW + (wn * FN * 16 + r) * 64 + ((q ^ ((r >> 2) & 3)) * 16));
+  const uint32_t wsrow = (uint32_t)(kScales + (wn * FN * 16 + r) * 16);
+  const uint32_t sel = (uint32_t)(q | ((q + 4) << 8)) | 0x0C0C0000u;
+
+  bf16x8 x[2][FM];                              // activation fragments of this step and the next
+  u32x4 w[FN], wn_[FN];                         // codes of this stage and the next
+  uint32_t sc[FN], scn[FN];                     // packed scale bytes of four stages, and the next four
+  auto read_x = [&](int buf, uint32_t slot, int v, int i) {
+    x[buf][i] = *reinterpret_cast<const bf16x8*>(smem + slot + xrow + i * 4096 + (uint32_t)(((4 * q + v) ^ r) * 16));
+  };
+  auto read_w = [&](uint32_t slot, int j) { return *reinterpret_cast<const u32x4*>(smem + slot + wfrag + j * 1024); };
+  auto read_scales = [&](int group, int j) {
+    return *reinterpret_cast<const u32x4*>(smem + (uint32_t)(group & 1) * kGroup4 + wsrow + j * 256);
+  };
+  auto shift_of = [&](int group) { return 8 * min(3, kt0 + 4 * group - group_start(group)); };
+
+  // One stage; J = stage % 4 selects the scale byte, J % 2 the slot.  The fragments of a step are read
+  // during the step before.  The last step of a stage waits for the next stage's
+  // copies, meets the other waves and starts refilling the slot; the copies go on into
+  // the next stage's first steps.
+  auto stage_steps = [&](auto jc, int s) {
+    constexpr int J = decltype(jc)::value;
+    constexpr uint32_t slot = (J & 1) * kSlot, other = kSlot - slot;
+    const int stage = s + J;
+    const bool last = rem != 0 && kt0 + stage == KT - 1;
+    if (last && q >= rem) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) w[j] = u32x4{0, 0, 0, 0};
+    }
+    Src src = source(stage + 1);                // what the previous stage's last step began
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int cur = v & 1;
+      if (v == 3) {
+        wait_vmcnt<0>();
+        mx_phase_barrier();
+        src = source(stage + 2);
+      }
+      if (last && q >= rem) {
+        // the other operand of a missing block is zero too: infinities times zero are NaN
+#pragma unroll
+        for (int i = 0; i < FM; ++i) x[cur][i] = __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0});
+      }
+      u32x4 raw[FN];
+      const int group = (stage + 1) >> 2, shift = J == 3 && v == 3 ? shift_of(group) : 0;
+      bf16x8 wv[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) wv[j] = mx_expand(w[j][v], mx_scale((sc[j] >> (8 * J)) & 255u));
+      // reads: the next step's activations; in the last step also the next stage's codes (and
+      // at the end of four stages scales), packed a few operations later
+      constexpr int kLag = 2;
+      const int kReads = FM + (v == 3 ? FN + (J == 3 ? FN + kLag : 0) : 0);
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const int tc = v == 3 ? t : (v + 1) * T + t;      // matrix instructions since the slot was free
+        if (tc % kEvery == 0 && tc / kEvery <= C) {
+          const int u = tc / kEvery;
+          if (u == 0) { if constexpr (J == 1) copy_scales((stage + 3) >> 2); }
+          else copy(src, v == 3 ? slot : other, u - 1);
+        }
+        const int per = (kReads + T - 1) / T;
+#pragma unroll
+        for (int o = t * per; o < (t + 1) * per && o < kReads; ++o) {
+          if (o < FM) {
+            if (v == 3) read_x(0, other, 0, o);
+            else read_x(cur ^ 1, slot, v + 1, o);
+          } else if (o < FM + FN) {
+            wn_[o - FM] = read_w(other, o - FM);
+          } else {
+            const int e = o - FM - FN;
+            if (e >= kLag) scn[e - kLag] = pack_bytes(raw[e - kLag], sel) >> shift;
+            if (e < FN) raw[e] = read_scales(group, e);
+          }
+        }
+        const int i = t / FN, j = t % FN;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j], x[cur][i], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      w[j] = wn_[j];
+      if constexpr (J == 3) sc[j] = scn[j];
+    }
+  };
+
+  constexpr int kEarly = (T - 1) / kEvery < C ? (T - 1) / kEvery : C;
+  copy_scales(0);
+  {
+    const Src s0 = source(0), s1 = source(1);
+#pragma unroll
+    for (int u = 0; u < C; ++u) copy(s0, 0, u);
+    // of stage 1 the copies that a last step would have issued; the first stage issues the rest
+#pragma unroll
+    for (int u = 0; u < kEarly; ++u) copy(s1, kSlot, u);
+  }
+  wait_vmcnt<kEarly>();
+  mx_phase_barrier();
+#pragma unroll
+  for (int i = 0; i < FM; ++i) read_x(0, 0, 0, i);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    w[j] = read_w(0, j);
+    sc[j] = pack_bytes(read_scales(0, j), sel) >> shift_of(0);
+  }
+  for (int s = 0; s < n_stages; s += 4) {
+    stage_steps(std::integral_constant<int, 0>{}, s);
+    if (s + 1 < n_stages) stage_steps(std::integral_constant<int, 1>{}, s);
+    if (s + 2 < n_stages) stage_steps(std::integral_constant<int, 2>{}, s);
+    if (s + 3 < n_stages) stage_steps(std::integral_constant<int, 3>{}, s);
+  }
+  wait_vmcnt<0>();
+  lds_barrier();                                // no copy and no read of the slots is left
+  mx_store_tile<FM, FN>(a, acc, m0 + wm * FM * 16, n0 + wn * FN * 16, smem + wave * kMxStage<FN>);
+}
+
+}  // namespace w4

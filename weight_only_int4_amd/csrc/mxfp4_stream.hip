@@ -1,17 +1,30 @@
 // Products with MXFP4 weights that read both operands straight into registers:
-// Y = X W_hat^T with bf16 activations (ACT = 16) or MXFP4 activations (ACT = 4).
+// Y = X W_hat^T with bf16 activations (ACT = 16) or MXFP4 activations (ACT = 4), for the
+// row counts at which the weights' bytes or plain latency are the bound.
 //
-// A workgroup owns 16 CB output channels and up to 16 RB activation rows; its waves
-// take the 128-channel steps of K in turn, each keeps its own fp32 tile, and the tiles
-// meet in LDS once, at the end, added in wave order (results are the same bit for bit
-// on every run).  The weights are the matrix instruction's row operand: lane (r, q)
-// holds the 16 bytes of block q of the step in channel r, which is one MX block with
-// one scale byte.
+// A workgroup owns CB tiles of 16 / SL output channels and up to 16 RB activation rows.
+// Its waves take the steps of K in turn, each keeps its own fp32 tile, and the tiles meet
+// in LDS once, at the end, added in wave order (results are the same bit for bit on
+// every run).  Loads of the next step are issued before the current one is multiplied.
+//
+// The weights are the matrix instruction's row operand: lane (r, q) holds 16 bytes, one MX
+// block with one scale byte.
 //   ACT = 16: each of the block's four words expands to eight bf16 (4 conversions,
 //     scale included, exact), the operand of one v_mfma_f32_16x16x32_bf16 whose other
 //     operand is the same 8 channels of an activation row: the lane's 64 bytes of
 //     activations are the four operands as they stand.
 //   ACT = 4: one v_mfma_scale_f32_16x16x128_f8f6f4 takes the block as it stands.
+// A step is SL slices of 128 channels of K for 16 / SL output channels: row operand r is
+// channel r / SL in slice r % SL, column c of the other operand activation row c / SL in
+// slice c % SL, and at the end the products of equal slices (r % SL == c % SL) are added.
+// A load of weights then covers 16 / SL rows of 64 SL contiguous bytes: with SL = 1 every
+// piece is half a cache line, which costs the L1 as much as a whole one, and there are
+// SL times as many tiles to spread over the CUs.  The price, SL times the matrix
+// instructions per row, is small change while the weights are the bound.
+// bf16 activations are loaded in whole rows (16 lanes to the 256 bytes of a slice) and
+// turned into operand order through 4 KB of LDS per wave: in operand order a load would be
+// 64 pieces of 16 bytes, four times the cache lines.  Chunk k of column c is at position k ^
+// c, so that both sides are free of bank conflicts.
 // Loads are range-checked buffer loads: rows past M and N and blocks past K read
 // zeros and touch no memory.
 #include <algorithm>
@@ -29,132 +42,287 @@ struct MxStreamArgs {
   const uint32_t* qweight;
   const uint8_t* scales;
   uint16_t* Y;
+  float* partial;         // [splits][M][N] when K is split over blockIdx.z, else NULL
+  int steps;              // steps of one split
 };
 
-template <int ACT, int RB, int CB>
-__global__ __launch_bounds__(512) void mx_stream_kernel(MxStreamArgs a) {
-  constexpr int kRow = 16 * CB + 4;            // floats of an LDS row, padded against bank conflicts
-  extern __shared__ float red[];               // [wave][16][kRow]
+// Sum over the SL neighbouring lanes of a slice group (1, 2 or 4 lanes).
+template <int SL>
+__device__ __forceinline__ float slice_sum(float v) {
+  if constexpr (SL >= 2)
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));   // lane ^ 1
+  if constexpr (SL >= 4)
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));   // lane ^ 2
+  return v;
+}
+
+constexpr int kMxStreamWaves = 4;              // at most, per workgroup
+constexpr int kMxTurn = 4096;                  // bytes per wave that turn activations into operand order
+
+template <int ACT, int SL, int RB, int CB>
+__global__ __launch_bounds__(kMxStreamWaves * 64) void mx_stream_kernel(MxStreamArgs a) {
+  constexpr int kCh = 16 / SL;                 // channels per tile, and activation rows per tile
+  constexpr int kRow = kCh * CB + 4;           // floats of an LDS row, padded against bank conflicts
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  float* red = reinterpret_cast<float*>(lds);  // [wave][kCh][kRow], after the last step
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   const int r = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16 * CB, m0 = blockIdx.y * 16 * RB;
+  const int n0 = blockIdx.x * kCh * CB, m0 = blockIdx.y * kCh * RB;
   const int KB = a.K / kMxBlock;
-  const int nrows = min(16 * CB, a.N - n0), mrows = min(16 * RB, a.M - m0);
+  const int nrows = min(kCh * CB, a.N - n0), mrows = min(kCh * RB, a.M - m0);
   const auto rw = make_rsrc(a.qweight + (size_t)n0 * (a.K / 8), (uint32_t)nrows * (uint32_t)(a.K / 2));
   const auto rs = make_rsrc(a.scales + (size_t)n0 * KB, (uint32_t)nrows * (uint32_t)KB);
   const auto rx = ACT == 16 ? make_rsrc(a.X + (size_t)m0 * a.K, (uint32_t)mrows * (uint32_t)a.K * 2u)
                             : make_rsrc(a.Xq + (size_t)m0 * (a.K / 8), (uint32_t)mrows * (uint32_t)(a.K / 2));
   const auto rxs = ACT == 16 ? rs : make_rsrc(a.xs + (size_t)m0 * KB, (uint32_t)mrows * (uint32_t)KB);
+  const int t0 = blockIdx.z * a.steps, t1 = min((KB + 4 * SL - 1) / (4 * SL), t0 + a.steps);
 
-  constexpr int XV = ACT == 16 ? 4 : 1;        // 16-byte loads of an activation row per step
+  constexpr int XV = ACT == 16 ? 4 : 1;        // 16-byte loads of an activation tile per lane and step
+  const uint32_t wo = (uint32_t)(r / SL) * (uint32_t)(a.K / 2), so = (uint32_t)(r / SL) * (uint32_t)KB;
+  const uint32_t wstep = (uint32_t)kCh * (uint32_t)(a.K / 2), sstep = (uint32_t)kCh * (uint32_t)KB;
+  const int kq = 4 * (r % SL) + q;             // block of this lane's weights within a step
+  // ACT = 16: load v of a tile covers columns 4 v + q, lane r its chunk r (8 channels);
+  // ACT = 4: the lane's own column r and block q.
+  uint32_t xo[XV];
+  int xk[XV];
+  const uint32_t xbytes = (uint32_t)(ACT == 16 ? a.K * 2 : a.K / 2);
+#pragma unroll
+  for (int v = 0; v < XV; ++v) {
+    const int c = ACT == 16 ? 4 * v + q : r;
+    xo[v] = (uint32_t)(c / SL) * xbytes + (ACT == 16 ? (uint32_t)(c % SL) * 256u + 16u * r : 16u * kq);
+    xk[v] = ACT == 16 ? 4 * (c % SL) + r / 4 : kq;
+  }
+  const uint32_t xtile = (uint32_t)kCh * xbytes;
+
+  struct Step {
+    u32x4 w[CB], x[RB][XV];
+    uint32_t ws[CB], xs[RB];
+  };
+  auto load = [&](int t, Step& s) {
+    const int left = t < t1 ? KB - 4 * SL * t : 0;       // blocks from this step on
+    const uint32_t kb = 4u * SL * (uint32_t)t;
+    const uint32_t wk = kq < left ? wo + 16u * (kb + kq) : kOob, sk = kq < left ? so + kb + kq : kOob;
+#pragma unroll
+    for (int j = 0; j < CB; ++j) {
+      s.w[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wk, (int)(j * wstep), 0));
+      s.ws[j] = __builtin_amdgcn_raw_buffer_load_b8(rs, sk, (int)(j * sstep), 0);
+    }
+#pragma unroll
+    for (int v = 0; v < XV; ++v) {
+      const uint32_t o = xk[v] < left ? xo[v] + (ACT == 16 ? 64u : 16u) * kb : kOob;
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+        s.x[i][v] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, o, (int)(i * xtile), 0));
+    }
+    if constexpr (ACT == 4) {
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+        s.xs[i] = __builtin_amdgcn_raw_buffer_load_b8(rxs, sk, (int)(i * sstep), 0);
+    }
+  };
+
   f32x4 acc[RB][CB];
 #pragma unroll
   for (int i = 0; i < RB; ++i)
 #pragma unroll
     for (int j = 0; j < CB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  const int steps = (KB + 3) / 4;
-  for (int t = wave; t < steps; t += waves) {
-    const int kb = 4 * t + q;
-    const bool ok = kb < KB;
-    u32x4 w[CB], x[RB][XV];
-    uint32_t ws[CB], xsc[RB];
+  unsigned char* turn = lds + wave * kMxTurn;
+  auto multiply = [&](const Step& s) {
+    if constexpr (ACT == 16) {
+      // LDS operations of one wave complete in order: no barrier between the tiles
+      bf16x8 x[RB][4];
 #pragma unroll
-    for (int j = 0; j < CB; ++j) {
-      const uint32_t row = (uint32_t)(16 * j + r);
-      w[j] = __builtin_bit_cast(
-          u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, ok ? row * (uint32_t)(a.K / 2) + 16u * kb : kOob, 0, 0));
-      ws[j] = __builtin_amdgcn_raw_buffer_load_b8(rs, ok ? row * (uint32_t)KB + (uint32_t)kb : kOob, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      const uint32_t row = (uint32_t)(16 * i + r);
-      const uint32_t xo = row * (uint32_t)(ACT == 16 ? a.K * 2 : a.K / 2) + (ACT == 16 ? 64u : 16u) * kb;
-#pragma unroll
-      for (int v = 0; v < XV; ++v)
-        x[i][v] = __builtin_bit_cast(u32x4,
-                                     __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? xo + 16u * v : kOob, 0, 0));
-      if constexpr (ACT == 4)
-        xsc[i] = __builtin_amdgcn_raw_buffer_load_b8(rxs, ok ? row * (uint32_t)KB + (uint32_t)kb : kOob, 0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < CB; ++j) {
-      if constexpr (ACT == 16) {
-        const float sc = mx_scale(ws[j]);
+      for (int i = 0; i < RB; ++i) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const bf16x8 wb = mx_expand(w[j][v], sc);
+          const int c = 4 * v + q;
+          *reinterpret_cast<u32x4*>(turn + c * 256 + ((r ^ c) * 16)) = s.x[i][v];
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          x[i][v] = *reinterpret_cast<const bf16x8*>(turn + r * 256 + (((4 * q + v) ^ r) * 16));
+        __builtin_amdgcn_wave_barrier();
+      }
+#pragma unroll
+      for (int j = 0; j < CB; ++j) {
+        const float sc = mx_scale(s.ws[j]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const bf16x8 wb = mx_expand(s.w[j][v], sc);
 #pragma unroll
           for (int i = 0; i < RB; ++i)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, __builtin_bit_cast(bf16x8, x[i][v]), acc[i][j], 0,
-                                                               0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, x[i][v], acc[i][j], 0, 0, 0);
         }
-      } else {
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
 #pragma unroll
         for (int i = 0; i < RB; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(w[j]), mx_operand(x[i][0]), acc[i][j],
-                                                                      4, 4, 0, (int)ws[j], 0, (int)xsc[i]);
-      }
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(s.w[j]), mx_operand(s.x[i][0]),
+                                                                      acc[i][j], 4, 4, 0, (int)s.ws[j], 0, (int)s.xs[i]);
     }
+  };
+  // two register sets take the steps in turn; loads past the end touch no memory
+  Step s0, s1;
+  load(t0 + wave, s0);
+  for (int t = t0 + wave; t < t1; t += 2 * waves) {
+    load(t + waves, s1);
+    multiply(s0);
+    if (t + waves >= t1) break;
+    load(t + 2 * waves, s0);
+    multiply(s1);
   }
 
-  // Tiles to LDS, 16 rows at a time: lane (c, q) holds row c, channels 16 j + 4 q .. + 3.
+  // Tiles to LDS, one row tile at a time.  Lane (c, q) of a tile holds column c and the tile's
+  // rows 4 q .. 4 q + 3: channel (4 q + e) / SL of activation row c / SL, of use where
+  // e % SL == c % SL.
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
-    if (i) __syncthreads();
-#pragma unroll
-    for (int j = 0; j < CB; ++j)
-      *reinterpret_cast<f32x4*>(&red[(wave * 16 + r) * kRow + 16 * j + 4 * q]) = acc[i][j];
     __syncthreads();
-    for (int o = threadIdx.x; o < 64 * CB; o += blockDim.x) {
-      const int row = o / (4 * CB), c = (o % (4 * CB)) * 4;
+    float* mine = red + (size_t)(wave * kCh + r / SL) * kRow;
+#pragma unroll
+    for (int j = 0; j < CB; ++j) {
+      const f32x4 v = acc[i][j];
+      if constexpr (SL == 1) {
+        *reinterpret_cast<f32x4*>(mine + 16 * j + 4 * q) = v;
+      } else if constexpr (SL == 2) {
+        const float e0 = slice_sum<2>(r & 1 ? v[1] : v[0]), e1 = slice_sum<2>(r & 1 ? v[3] : v[2]);
+        if ((r & 1) == 0) *reinterpret_cast<float2*>(mine + 8 * j + 2 * q) = make_float2(e0, e1);
+      } else {
+        const float lo = r & 1 ? v[1] : v[0], hi = r & 1 ? v[3] : v[2];
+        const float e0 = slice_sum<4>(r & 2 ? hi : lo);
+        if ((r & 3) == 0) mine[4 * j + q] = e0;
+      }
+    }
+    __syncthreads();
+    constexpr int kQuads = kCh * CB / 4;       // groups of four channels per row
+    for (int o = threadIdx.x; o < kCh * kQuads; o += blockDim.x) {
+      const int row = o / kQuads, c = (o % kQuads) * 4;
       f32x4 sum = *reinterpret_cast<const f32x4*>(&red[row * kRow + c]);
       for (int wv = 1; wv < waves; ++wv) {
-        const f32x4 p = *reinterpret_cast<const f32x4*>(&red[(wv * 16 + row) * kRow + c]);
+        const f32x4 p = *reinterpret_cast<const f32x4*>(&red[(wv * kCh + row) * kRow + c]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] += p[e];
       }
-      const int m = m0 + 16 * i + row, n = n0 + c;
-      if (m < a.M) {
+      const int m = m0 + kCh * i + row, n = n0 + c;
+      if (m >= a.M) continue;
+      const size_t at = (size_t)m * a.N + n;
+      if (a.partial) {
+        float* p = a.partial + (size_t)blockIdx.z * a.M * a.N + at;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (n + e < a.N) a.Y[(size_t)m * a.N + n + e] = __builtin_bit_cast(uint16_t, (__bf16)sum[e]);
+          if (n + e < a.N) p[e] = sum[e];
+      } else if ((a.N & 3) == 0) {             // four whole, aligned outputs
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        if (n < a.N)
+          *reinterpret_cast<bf16x4*>(a.Y + at) = bf16x4{(__bf16)sum[0], (__bf16)sum[1], (__bf16)sum[2], (__bf16)sum[3]};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < a.N) a.Y[at + e] = __builtin_bit_cast(uint16_t, (__bf16)sum[e]);
       }
     }
   }
 }
 
-template <int ACT, int RB, int CB>
-int launch_stream(const MxStreamArgs& a, hipStream_t stream) {
-  const int steps = (a.K / kMxBlock + 3) / 4;
-  const int waves = std::min(8, steps);
-  const long long gx = (a.N + 16 * CB - 1) / (16 * CB), gy = (a.M + 16LL * RB - 1) / (16 * RB);
+template <int ACT, int SL, int RB, int CB>
+int launch_stream(const MxStreamArgs& base, int waves, int splits, hipStream_t stream) {
+  MxStreamArgs a = base;
+  const int steps = (a.K / kMxBlock + 4 * SL - 1) / (4 * SL);
+  a.steps = (steps + splits - 1) / splits;
+  const int nc = 16 / SL * CB;
+  const int mr = 16 / SL * RB;
+  const long long gx = (a.N + nc - 1LL) / nc, gy = (a.M + mr - 1LL) / mr;
   if (gy > 65535) return W4_ERR_SHAPE;
-  const size_t lds = (size_t)waves * 16 * (16 * CB + 4) * sizeof(float);
-  hipLaunchKernelGGL((mx_stream_kernel<ACT, RB, CB>), dim3((unsigned)gx, (unsigned)gy), dim3(waves * 64), lds, stream, a);
+  const size_t lds =
+      std::max<size_t>((size_t)waves * (16 / SL) * (nc + 4) * sizeof(float), ACT == 16 ? waves * kMxTurn : 0);
+  hipLaunchKernelGGL((mx_stream_kernel<ACT, SL, RB, CB>), dim3((unsigned)gx, (unsigned)gy, (unsigned)splits),
+                     dim3(waves * 64), lds, stream, a);
   W4_CHECK_LAUNCH();
   return W4_OK;
 }
 
 }  // namespace
 
+namespace {
+
+template <int ACT, int SL, int RB>
+int launch_cols(const MxStreamArgs& a, const MxStreamPlan& p, hipStream_t stream) {
+  switch (p.cols) {
+    case 1: return launch_stream<ACT, SL, RB, 1>(a, p.waves, p.splits, stream);
+    case 2: return launch_stream<ACT, SL, RB, 2>(a, p.waves, p.splits, stream);
+    default: return launch_stream<ACT, SL, RB, 4>(a, p.waves, p.splits, stream);
+  }
+}
+
+template <int ACT>
+int launch_act(const MxStreamArgs& a, const MxStreamPlan& p, hipStream_t stream) {
+  if (p.slices == 4) return launch_cols<ACT, 4, 1>(a, p, stream);
+  if (p.slices == 2) {
+    switch (p.rows) {
+      case 1: return launch_cols<ACT, 2, 1>(a, p, stream);
+      case 2: return launch_cols<ACT, 2, 2>(a, p, stream);
+      default: return launch_cols<ACT, 2, 3>(a, p, stream);
+    }
+  }
+  switch (p.rows) {
+    case 1: return launch_cols<ACT, 1, 1>(a, p, stream);
+    case 2: return launch_cols<ACT, 1, 2>(a, p, stream);
+    case 3: return launch_cols<ACT, 1, 3>(a, p, stream);
+    default: return launch_cols<ACT, 1, 4>(a, p, stream);
+  }
+}
+
+}  // namespace
+
+MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N) {
+  (void)act_bits;
+  MxStreamPlan p{};
+  const bool large = (long long)N * K >= (32LL << 20);
+  p.slices = M <= 4 ? 4 : M <= 8 || (large && M <= 24) ? 2 : 1;
+  p.rows = std::min(4, (M * p.slices + 15) / 16);
+  const int steps = (K / kMxBlock + 4 * p.slices - 1) / (4 * p.slices);
+  const long long tiles = (N + 16LL / p.slices - 1) / (16 / p.slices) * ((M + 16LL * p.rows / p.slices - 1) / (16 * p.rows / p.slices));
+  p.cols = tiles >= 1024 && M > 8 ? 4 : tiles >= 512 ? 2 : 1;
+  p.splits = 1;
+  if (M > 24 && steps >= 32 && tiles <= 256) {
+    p.cols = 2;
+    p.splits = 4;
+  }
+  const long long wgs = (tiles + p.cols - 1) / p.cols * p.splits;
+  p.waves = wgs <= 512 ? 4 : wgs <= 1280 ? 2 : 1;
+  while (p.waves > 1 && 2 * p.waves * p.splits > steps) p.waves /= 2;
+  return p;
+}
+
+int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t stream) {
+  MxStreamArgs a{g.X, g.Xq, g.xscales, g.M, g.K, g.N, g.qweight, g.scales, g.Y,
+                 p.splits > 1 ? static_cast<float*>(g.workspace) : nullptr, 0};
+  const int st = g.act_bits == 16 ? launch_act<16>(a, p, stream) : launch_act<4>(a, p, stream);
+  if (st || p.splits == 1) return st;
+  const size_t MN = (size_t)g.M * g.N;
+  return launch_split_reduce(a.partial, p.splits, MN, MN, g.Y, stream);
+}
+
+bool mxfp4_use_tile(int act_bits, int M, int K, int N) {
+  (void)act_bits; (void)K; (void)N;
+  return M > 64;
+}
+
 size_t mxfp4_gemm_workspace_bytes(int act_bits, int M, int K, int N) {
-  (void)act_bits; (void)M; (void)K; (void)N;
-  return 0;
+  if (M == 0 || N == 0) return 0;
+  if (mxfp4_use_tile(act_bits, M, K, N)) return mx_tile_workspace_bytes(plan_mx_tile(act_bits, M, K, N), act_bits, M, K, N);
+  const MxStreamPlan p = plan_mx_stream(act_bits, M, K, N);
+  return p.splits > 1 ? (size_t)p.splits * M * N * sizeof(float) : 0;
 }
 
 int launch_mxfp4_gemm(const MxGemmArgs& g, hipStream_t stream) {
-  MxStreamArgs a{g.X, g.Xq, g.xscales, g.M, g.K, g.N, g.qweight, g.scales, g.Y};
-  if (g.act_bits == 16) {
-    if (g.M <= 16) return launch_stream<16, 1, 1>(a, stream);
-    if (g.M <= 32) return launch_stream<16, 2, 4>(a, stream);
-    return launch_stream<16, 4, 4>(a, stream);
-  }
-  if (g.M <= 16) return launch_stream<4, 1, 1>(a, stream);
-  if (g.M <= 32) return launch_stream<4, 2, 4>(a, stream);
-  return launch_stream<4, 4, 4>(a, stream);
+  if (mxfp4_use_tile(g.act_bits, g.M, g.K, g.N)) return launch_mx_tile(plan_mx_tile(g.act_bits, g.M, g.K, g.N), g, stream);
+  return launch_mx_stream(plan_mx_stream(g.act_bits, g.M, g.K, g.N), g, stream);
 }
 
 }  // namespace w4
