@@ -576,6 +576,10 @@ def gemm_launcher(X, qweight, scales, qzeros, symmetric: bool, Y, workspace=None
 
 
 def _mx_need(t, dtype, name, shape, device):
+    # one test on the way through; the reason is found out afterwards
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return
     _need(t, dtype, name, len(shape))
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
@@ -583,13 +587,21 @@ def _mx_need(t, dtype, name, shape, device):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
-def _mx_call(fn, args, device):
+# the calls behind torch.cuda.current_device() and current_stream().cuda_stream, without
+# the objects built around them (2 us of a 6 us launch)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _mx_call(fn, args, index):
     # kernels go to the current device: make it the tensors' own for the call
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(device)))
+    if index == _current_device():
+        rc = fn(*args, _current_raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(device)))
+        with torch.cuda.device(index):
+            rc = fn(*args, _current_raw_stream(index))
+    if rc:
+        _check(rc)
 
 
 def _mx_width(t, per, name):
@@ -618,7 +630,8 @@ def mxfp4_quantize(W, s=None, codes=None, scales=None):
         scales = torch.empty((N, K // MX_BLOCK), dtype=torch.uint8, device=dev)
     else:
         _mx_need(scales, torch.uint8, "scales", (N, K // MX_BLOCK), dev)
-    _mx_call(lib.mxfp4_quantize, (_ptr(W), N, K, _ptr(s), _ptr(codes), _ptr(scales)), dev)
+    _mx_call(lib.mxfp4_quantize, (W.data_ptr(), N, K, None if s is None else s.data_ptr(), codes.data_ptr(),
+                                  scales.data_ptr()), dev.index)
     return codes, scales
 
 
@@ -633,7 +646,7 @@ def mxfp4_dequantize(codes, scales, W=None):
         W = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
     else:
         _mx_need(W, torch.bfloat16, "W", (N, K), dev)
-    _mx_call(lib.mxfp4_dequantize, (_ptr(codes), _ptr(scales), N, K, _ptr(W)), dev)
+    _mx_call(lib.mxfp4_dequantize, (codes.data_ptr(), scales.data_ptr(), N, K, W.data_ptr()), dev.index)
     return W
 
 
@@ -665,9 +678,10 @@ def _mx_gemm_launcher(cname, acts, qweight, scales, Y, workspace):
     ws, wsb = _workspace(q, dev, workspace)
     args = (*map(_ptr, acts), M, K, N, _ptr(qweight), _ptr(scales), _ptr(Y), _ptr(ws),
             None if wsb is None else ctypes.byref(wsb))
+    index = dev.index
 
     def launch():
-        _mx_call(fn, args, dev)
+        _mx_call(fn, args, index)
 
     launch.tensors = (*acts, qweight, scales, Y, ws)     # kept alive while the launcher is
     launch.workspace_size = wsb

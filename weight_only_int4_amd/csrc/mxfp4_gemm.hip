@@ -9,13 +9,16 @@ namespace w4 {
 namespace {
 
 // Scale rows padded to `to` bytes with zeros (a scale of 2^-127 for blocks whose codes
-// are zero).
-__global__ __launch_bounds__(256) void mx_pad_scales_kernel(const uint8_t* from, int rows, int kb, uint8_t* out, int to) {
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (size_t)rows * to) return;
-  const size_t row = i / to;
-  const int b = (int)(i % to);
-  out[i] = b < kb ? from[row * kb + b] : 0;
+// are zero): the weights' rows, then the activations'.
+__global__ __launch_bounds__(256) void mx_pad_scales_kernel(const uint8_t* w, int N, const uint8_t* x, int M, int kb,
+                                                            uint8_t* wout, uint8_t* xout, int to) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, nw = (size_t)N * to;
+  if (i >= nw + (size_t)M * to) return;
+  const uint8_t* from = i < nw ? w : x;
+  uint8_t* out = i < nw ? wout : xout;
+  const size_t at = i < nw ? i : i - nw, row = at / to;
+  const int b = (int)(at % to);
+  out[at] = b < kb ? from[row * kb + b] : 0;
 }
 
 // A tile shape with what it costs: microseconds per workgroup (start, first copies, stores)
@@ -27,8 +30,8 @@ struct MxTile {
   float start, alone, full;
 };
 constexpr MxTile kTiles4[] = {{256, 256, 1, 7.0f, 0.90f, 0.90f}, {256, 192, 1, 5.0f, 0.75f, 0.75f},
-                              {128, 128, 2, 2.6f, 0.27f, 0.65f}, {128, 64, 2, 1.8f, 0.21f, 0.48f},
-                              {64, 64, 4, 1.5f, 0.18f, 0.59f}};
+                              {128, 128, 2, 3.0f, 0.36f, 0.65f}, {128, 64, 2, 1.8f, 0.28f, 0.48f},
+                              {64, 64, 4, 1.5f, 0.25f, 0.59f}};
 constexpr MxTile kTiles16[] = {{256, 192, 1, 6.0f, 2.50f, 2.50f}, {128, 128, 1, 3.2f, 0.88f, 1.03f},
                                {128, 64, 2, 2.4f, 0.62f, 1.10f}, {64, 64, 3, 1.7f, 0.50f, 1.20f}};
 constexpr int kCus = 256;
@@ -74,10 +77,11 @@ MxTilePlan plan_mx_tile(int act_bits, int M, int K, int N) {
 }
 
 // Workspace: padded scale rows of the weights and of the activations, partial outputs.
+namespace {
 struct MxTileLayout {
   size_t w, x, partial, total;
 };
-static MxTileLayout tile_layout(const MxTilePlan& p, int act_bits, int M, int K, int N) {
+MxTileLayout tile_layout(const MxTilePlan& p, int act_bits, int M, int K, int N) {
   const int ss = padded_scale_row(K / kMxBlock);
   MxTileLayout l{};
   l.x = align_up((size_t)N * ss, 256);
@@ -85,6 +89,7 @@ static MxTileLayout tile_layout(const MxTilePlan& p, int act_bits, int M, int K,
   l.total = l.partial + (p.splits > 1 ? (size_t)p.splits * M * N * sizeof(float) : 0);
   return l;
 }
+}  // namespace
 
 size_t mx_tile_workspace_bytes(const MxTilePlan& p, int act_bits, int M, int K, int N) {
   return tile_layout(p, act_bits, M, K, N).total;
@@ -107,13 +112,13 @@ int launch_mx_tile(const MxTilePlan& p, const MxGemmArgs& g, hipStream_t stream)
   a.Y = g.Y;
   a.partial = p.splits > 1 ? reinterpret_cast<float*>(ws + l.partial) : nullptr;
   if (ss) {
-    auto pad = [&](const uint8_t* from, int rows, size_t at) {
-      const size_t blocks = ((size_t)rows * ss + 255) / 256;
-      hipLaunchKernelGGL(mx_pad_scales_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, from, rows, KB, ws + at, ss);
-      return static_cast<const uint8_t*>(ws + at);
-    };
-    a.ws = pad(g.scales, g.N, l.w);
-    if (g.act_bits == 4) a.xs = pad(g.xscales, g.M, l.x);
+    const int rows = g.act_bits == 4 ? g.M : 0;
+    const size_t blocks = ((size_t)(g.N + (long long)rows) * ss + 255) / 256;
+    if (blocks > 0x7FFFFFFFu) return W4_ERR_SHAPE;
+    hipLaunchKernelGGL(mx_pad_scales_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, g.scales, g.N, g.xscales, rows,
+                       KB, ws + l.w, ws + l.x, ss);
+    a.ws = ws + l.w;
+    a.xs = ws + l.x;
     a.ss = ss;
   }
   const MxTile& t = g.act_bits == 4 ? kTiles4[p.tile] : kTiles16[p.tile];

@@ -279,23 +279,38 @@ int launch_act(const MxStreamArgs& a, const MxStreamPlan& p, hipStream_t stream)
 
 }  // namespace
 
+// Rules from a sweep of every form over hidden-2048 and 27B-shaped linears, 1 to 64 rows
+// (microseconds, chosen against the other side):
+//  * Slices: 4 up to 4 rows, 2 up to 8.  For 9 to 16 rows (24 with bf16 activations) two
+//    slices pay where rows of weights are long: K = 6144, N = 2048, 16 rows 5.9 against 6.5,
+//    K = 5120, N = 17408 16.5 against 18; at K = 2048 one slice with bf16 activations, 3.7
+//    against 4.1.
+//  * Channel tiles per workgroup: more of them share the activations, fewer fill the
+//    CUs.  M = 16: 640 tiles 18.5 with four against 21.8 with two, 384 tiles 4.6 with two against
+//    5.3 with one, 256 tiles 5.9 with one against 6.6 with two.  From 25 rows on two (registers).
+//  * Waves: with few workgroups the waves split K four ways; many workgroups need none of it
+//    (M = 1, K = 5120, N = 17408: 10.2 with one against 11.4 with four).
+//  * K is split over workgroups, with a second launch, where few tiles meet a long K: M = 37,
+//    K = 6144, N = 2048 9.1 against 10.7.
 MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N) {
-  (void)act_bits;
   MxStreamPlan p{};
-  const bool large = (long long)N * K >= (32LL << 20);
-  p.slices = M <= 4 ? 4 : M <= 8 || (large && M <= 24) ? 2 : 1;
+  p.slices = M <= 4 ? 4 : M <= 8 ? 2 : act_bits == 4 ? (M <= 16 ? 2 : 1) : (M <= 24 && K >= 4096 ? 2 : 1);
   p.rows = std::min(4, (M * p.slices + 15) / 16);
+  const int ch = 16 / p.slices;                 // channels per tile, and activation rows per tile
   const int steps = (K / kMxBlock + 4 * p.slices - 1) / (4 * p.slices);
-  const long long tiles = (N + 16LL / p.slices - 1) / (16 / p.slices) * ((M + 16LL * p.rows / p.slices - 1) / (16 * p.rows / p.slices));
-  p.cols = tiles >= 1024 && M > 8 ? 4 : tiles >= 512 ? 2 : 1;
+  const long long tiles = (N + ch - 1LL) / ch * ((M + (long long)ch * p.rows - 1) / (ch * p.rows));
+  if (M <= 4) p.cols = tiles >= 512 ? 2 : 1;
+  else if (M <= 8) p.cols = tiles >= 2048 ? 2 : tiles >= 512 ? 4 : 1;
+  else if (M <= 24) p.cols = tiles >= 512 ? 4 : tiles >= 320 ? 2 : 1;
+  else p.cols = tiles >= 320 ? 2 : 1;
   p.splits = 1;
   if (M > 24 && steps >= 32 && tiles <= 256) {
     p.cols = 2;
     p.splits = 4;
   }
   const long long wgs = (tiles + p.cols - 1) / p.cols * p.splits;
-  p.waves = wgs <= 512 ? 4 : wgs <= 1280 ? 2 : 1;
-  while (p.waves > 1 && 2 * p.waves * p.splits > steps) p.waves /= 2;
+  p.waves = wgs <= 512 ? 4 : wgs <= 1280 && M <= 24 ? 2 : 1;
+  while (p.waves > 1 && 2 * p.waves * p.splits > steps) p.waves /= 2;   // two steps a wave at least
   return p;
 }
 
@@ -308,9 +323,18 @@ int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t str
   return launch_split_reduce(a.partial, p.splits, MN, MN, g.Y, stream);
 }
 
+// The tiled form with 4-bit activations from 17 rows on (K = 2048, N = 6144: M = 20 5.4 against 5.8,
+// M = 64 5.6 against 9.0), 33 on small weights (K = N = 2048, M = 20: 5.3 against 4.8); with bf16
+// ones where more than 32 rows and 10^9 products meet (K = 2048, N = 6144: M = 64 11.1 against
+// 9.0, M = 128 12.3 against 15.9; K = 5120, N = 17408: M = 32 29 against 24, M = 64 33 against 35).
+// Where scale rows have to be padded first, by another launch, it has to be worth that
+// (4-bit, M = 333, K = 1056, N = 2047: 7.8 here against 9.5).
 bool mxfp4_use_tile(int act_bits, int M, int K, int N) {
-  (void)act_bits; (void)K; (void)N;
-  return M > 64;
+  const long long NK = (long long)N * K, MNK = M * NK;
+  if (act_bits == 16) return M > 32 && MNK >= 1000000000LL;
+  const int KB = K / kMxBlock;
+  if (KB % 4 != 0 || KB < 16) return MNK >= 2000000000LL;
+  return M > (NK >= (8LL << 20) ? 16 : 32);
 }
 
 size_t mxfp4_gemm_workspace_bytes(int act_bits, int M, int K, int N) {
