@@ -37,6 +37,12 @@ __device__ __forceinline__ bf16x8 mx_expand(uint32_t w, float scale) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
+// Position of chunk 0 in row r (0..15) of 256-byte LDS rows read as operands: lane (r, q) reads
+// chunk 4 q + v of row r, 16 bytes, and an LDS pass takes lanes 0-3, 12-15, 20-27 (then 4-11,
+// 16-19, 28-31, and the same of the upper half), so that rows 4-11 meet the other rows' chunk
+// with bit 2 flipped: flipped back, the pass covers 16 positions.
+__device__ __forceinline__ int mx_swizzle16(int r) { return r ^ ((((r >> 2) ^ (r >> 3)) & 1) << 2); }
+
 // 16 bytes of e2m1 codes as a matrix operand (the upper half of the register group is
 // not read for 4-bit elements).
 __device__ __forceinline__ i32x8 mx_operand(u32x4 w) {

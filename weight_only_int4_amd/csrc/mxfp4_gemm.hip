@@ -29,11 +29,11 @@ struct MxTile {
   int bm, bn, occ;
   float start, alone, full;
 };
-constexpr MxTile kTiles4[] = {{256, 256, 1, 7.0f, 0.90f, 0.90f}, {256, 192, 1, 5.0f, 0.75f, 0.75f},
-                              {128, 128, 2, 3.0f, 0.36f, 0.65f}, {128, 64, 2, 1.8f, 0.28f, 0.48f},
-                              {64, 64, 4, 1.5f, 0.25f, 0.59f}};
-constexpr MxTile kTiles16[] = {{256, 192, 1, 6.0f, 2.50f, 2.50f}, {128, 128, 1, 3.2f, 0.88f, 1.03f},
-                               {128, 64, 2, 2.4f, 0.62f, 1.10f}, {64, 64, 3, 1.7f, 0.50f, 1.20f}};
+constexpr MxTile kTiles4[] = {{256, 256, 1, 7.0f, 0.87f, 0.87f}, {256, 192, 1, 5.5f, 0.67f, 0.67f},
+                              {128, 128, 2, 3.0f, 0.36f, 0.54f}, {128, 64, 2, 2.0f, 0.27f, 0.37f},
+                              {64, 64, 4, 1.5f, 0.25f, 0.45f}};
+constexpr MxTile kTiles16[] = {{256, 192, 1, 6.0f, 2.48f, 2.48f}, {128, 128, 1, 3.2f, 0.88f, 0.97f},
+                               {128, 64, 2, 2.4f, 0.62f, 1.03f}, {64, 64, 3, 1.7f, 0.50f, 1.16f}};
 constexpr int kCus = 256;
 
 double tile_cost(const MxTile& t, long long wgs, int stages) {

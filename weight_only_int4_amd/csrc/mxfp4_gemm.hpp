@@ -15,12 +15,12 @@
 //
 // LDS layout: a row of codes is 64 bytes of a stage, chunk q (16 bytes) one MX block;
 // position p of row r holds chunk p ^ ((r >> 2) & 3).  A row of bf16 activations is 256
-// bytes, position p holding chunk p ^ (r & 15).  A 16-lane pass of fragment reads (16
-// rows, one chunk) then covers all 64 banks once.
+// bytes, position p holding chunk p ^ mx_swizzle16(r & 15).  Every pass of a fragment read
+// then covers all 64 banks once.
 //
-// Scale bytes come 16 at a time (four stages of a row, one 16-byte LDS read): an LDS
-// read of one byte per lane costs nearly as much as one of 16 (2.9 against 3.5 ns per
-// wave).  Lane (r, q) keeps byte q of each stage's dword, packed into one register.
+// Scale bytes are read 16 at a time (four stages of a row): an LDS read of one byte per
+// lane costs nearly as much as one of 16 (2.9 against 3.5 ns per wave).  Lane (r, q) keeps
+// byte q of each stage's dword, packed into one register.
 //
 // Rows past M or N re-read the last row (their outputs are not stored).  When K is not a
 // multiple of 128, copies of the last stage clamp to the blocks that exist and the lanes
@@ -126,11 +126,10 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   static_assert(BM % 64 == 0 && BN % 64 == 0, "copies and scale copies cover 64 rows");
   constexpr int FM = BM / 32, FN = BN / 32, F = FM + FN, T = FM * FN;
   constexpr int kRows = BM + BN;                // activation rows, then channels
-  constexpr int kSlot = kRows * 128, kScales = 2 * kSlot, kGroup4 = kRows * 16;
+  constexpr int kSlot = kRows * 128, kScales = 2 * kSlot;
   constexpr int C = kRows / 8 / W;              // 1 KB copies (8 rows) per wave and pair of stages
-  constexpr int kSUnits = kRows / 64;           // 1 KB copies per four stages of scales
-  constexpr int CS = (kSUnits + W - 1) / W;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * kSlot + 2 * kGroup4];
+  constexpr int CS = kRows / 16 / W;            // 1 KB copies (16 rows) per wave and 16 stages of scales
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * kSlot + kRows * 64];
   constexpr int kEvery = T / C;                 // matrix instructions per copy
   static_assert(kEvery >= 1 && C * kEvery < 2 * T, "a pair's copies fit two steps");
   const int lane = threadIdx.x & 63;
@@ -165,10 +164,8 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   }
 #pragma unroll
   for (int u = 0; u < CS; ++u) {
-    const int unit = min(wave + W * u, kSUnits - 1);
-    const bool isx = unit < BM / 64;
-    const int row = unit * 64 + lane - (isx ? 0 : BM);
-    soff[u] = (uint32_t)min(row, isx ? mlast : nlast) * (uint32_t)a.ss;
+    const int row = (wave + W * u) * 16 + (lane >> 2) - (u < BM / 16 / W ? 0 : BM);
+    soff[u] = (uint32_t)min(row, u < BM / 16 / W ? mlast : nlast) * (uint32_t)a.ss;
   }
   const int chunk = (lane & 7) ^ (((wave * 8 + (lane >> 3)) >> 1) & 7);
   // Copies of pair p of stages counted from kt0, into slot p % 2; past the end the last
@@ -184,16 +181,16 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   auto copy = [&](const Src& s, int slot, int u) {
     lds_copy16(off[u] + s.c, is_x(u) ? s.x : s.w, smem_base + (uint32_t)(slot * kSlot + (wave + W * u) * 1024));
   };
-  // A group's first stage, moved back where the row ends before the group does.
+  // A group's (four stages') first stage, moved back where the row ends before the group does.
   auto group_start = [&](int group) { return max(0, min(kt0 + 4 * group, KT - 4)); };
-  auto copy_scales = [&](int group) {
-    const int ks = group_start(group);
+  // Scales of groups 4 b .. 4 b + 3: 64 bytes of a row, four lanes to a row, position p of row r
+  // holding group 4 b + (p ^ ((r >> 2) & 3)).  (16 bytes of a row at a time would cost the L1 four
+  // times the lines, a third of what the codes cost.)
+  auto copy_scales = [&](int b) {
+    const uint32_t c = 4u * (uint32_t)group_start(4 * b + ((lane & 3) ^ ((lane >> 4) & 3)));
 #pragma unroll
-    for (int u = 0; u < CS; ++u) {
-      const int unit = min(wave + W * u, kSUnits - 1);
-      lds_copy16(soff[u], (unit < BM / 64 ? xsb : wsb) + (size_t)ks * 4,
-                 smem_base + kScales + (uint32_t)(group & 1) * kGroup4 + unit * 1024);
-    }
+    for (int u = 0; u < CS; ++u)
+      lds_copy16(soff[u] + c, u < BM / 16 / W ? xsb : wsb, smem_base + (uint32_t)(kScales + (wave + W * u) * 1024));
   };
 
   f32x4 acc[FM][FN];
@@ -206,8 +203,8 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   const uint32_t swz = (uint32_t)((q ^ ((r >> 1) & 7)) * 16);
   const uint32_t xfrag = (uint32_t)((wm * FM * 16 + r) * 128) + swz;
   const uint32_t wfrag = (uint32_t)((BM + wn * FN * 16 + r) * 128) + swz;
-  const uint32_t xsrow = (uint32_t)(kScales + (wm * FM * 16 + r) * 16);
-  const uint32_t wsrow = (uint32_t)(kScales + (BM + wn * FN * 16 + r) * 16);
+  const uint32_t xsrow = (uint32_t)(kScales + (wm * FM * 16 + r) * 64);
+  const uint32_t wsrow = (uint32_t)(kScales + (BM + wn * FN * 16 + r) * 64);
   const uint32_t sel = (uint32_t)(q | ((q + 4) << 8)) | 0x0C0C0000u;
 
   u32x4 f[2][F];                                // fragments of this stage and the next
@@ -218,8 +215,8 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
     f[buf][e] = *reinterpret_cast<const u32x4*>(smem + (j4 >> 1) * kSlot + o);
   };
   auto read_scales = [&](int group, int e) {
-    const uint32_t o = e < FN ? wsrow + e * 256 : xsrow + (e - FN) * 256;
-    return *reinterpret_cast<const u32x4*>(smem + (uint32_t)(group & 1) * kGroup4 + o);
+    const uint32_t o = e < FN ? wsrow + e * 1024 : xsrow + (e - FN) * 1024;
+    return *reinterpret_cast<const u32x4*>(smem + o + (uint32_t)(((group & 3) ^ ((r >> 2) & 3)) * 16));
   };
   auto shift_of = [&](int group) { return 8 * min(3, kt0 + 4 * group - group_start(group)); };
 
@@ -256,7 +253,8 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
       if (tc % kEvery == 0 && tc / kEvery < kCopies) {
         const int u = tc / kEvery;
         constexpr int slot = cur == 1 ? J >> 1 : (J >> 1) ^ 1;
-        if (u == 0) { if constexpr (J == 1 || J == 2) copy_scales((stage + 3) >> 2); }
+        // the last group of the scales in LDS is in registers by now
+        if (u == 0) { if (J == 1 && ((stage + 3) & 15) == 0) copy_scales((stage + 3) >> 4); }
         else copy(src, slot, u - 1);
       }
 #pragma unroll
@@ -318,10 +316,10 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a16_kernel(MxTileArgs a) {
   static_assert(BM % 64 == 0 && BN % 64 == 0, "copies and scale copies cover 64 rows");
   constexpr int FM = BM / 32, FN = BN / 32, T = FM * FN;
   constexpr int kX = 0, kW = BM * 256, kSlot = kW + BN * 64;
-  constexpr int kScales = 2 * kSlot, kGroup4 = BN * 16;
+  constexpr int kScales = 2 * kSlot;
   constexpr int CX = BM / 4 / W, CW = BN / 16 / W, C = CX + CW;   // 1 KB copies per wave and stage
-  constexpr int kSUnits = BN / 64, CS = (kSUnits + W - 1) / W;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * kSlot + 2 * kGroup4];
+  constexpr int kSUnits = BN / 32, CS = (kSUnits + W - 1) / W;    // 1 KB copies (32 rows) per wave and 8 stages of scales
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * kSlot + BN * 32];
   constexpr int kEvery = 2 * T / C;             // matrix instructions per copy: over two of the four steps
   static_assert(kEvery >= 1 && C * kEvery < 4 * T, "a stage's copies fit its steps");
   const int lane = threadIdx.x & 63;
@@ -343,7 +341,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a16_kernel(MxTileArgs a) {
   const int mlast = a.M - 1 - m0, nlast = a.N - 1 - n0;
 
   // Activation copy u: rows 4 (wave + 4 u) + lane / 16, position lane % 16 holding chunk
-  // (lane % 16) ^ (row & 15), and row & 15 is the same for every u.  Code copy u: rows
+  // (lane % 16) ^ mx_swizzle16(row & 15), and row & 15 is the same for every u.  Code copy u: rows
   // 16 (wave + 4 u) + lane / 4, position lane % 4 holding chunk (lane % 4) ^ ((row >> 2) & 3).
   uint32_t xoff[CX], woff[CW], soff[CS];
 #pragma unroll
@@ -351,8 +349,9 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a16_kernel(MxTileArgs a) {
 #pragma unroll
   for (int u = 0; u < CW; ++u) woff[u] = (uint32_t)min((wave + W * u) * 16 + (lane >> 2), nlast) * wrowb;
 #pragma unroll
-  for (int u = 0; u < CS; ++u) soff[u] = (uint32_t)min(min(wave + W * u, kSUnits - 1) * 64 + lane, nlast) * (uint32_t)a.ss;
-  const int xchunk = (lane & 15) ^ ((wave * 4 + (lane >> 4)) & 15), wchunk = (lane & 3) ^ ((lane >> 4) & 3);
+  for (int u = 0; u < CS; ++u)
+    soff[u] = (uint32_t)min(min(wave + W * u, kSUnits - 1) * 32 + (lane >> 1), nlast) * (uint32_t)a.ss;
+  const int xchunk = (lane & 15) ^ mx_swizzle16((wave * 4 + (lane >> 4)) & 15), wchunk = (lane & 3) ^ ((lane >> 4) & 3);
   // Copies of a stage counted from kt0 into slot stage % 2; past the end the last stage is
   // copied again, into a slot that nothing reads any more.
   struct Src {
@@ -369,14 +368,14 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a16_kernel(MxTileArgs a) {
     if (u < CX) lds_copy16(xoff[u] + s.cx, s.x, smem_base + slot + (uint32_t)(kX + (wave + W * u) * 1024));
     else lds_copy16(woff[u - CX] + s.cw, s.w, smem_base + slot + (uint32_t)(kW + (wave + W * (u - CX)) * 1024));
   };
-  // A group's first stage, moved back where the row ends before the group does.
+  // Groups of four stages as above; scales of groups 2 b and 2 b + 1, 32 bytes of a row, position
+  // p of row r holding group 2 b + (p ^ ((r >> 3) & 1)).
   auto group_start = [&](int group) { return max(0, min(kt0 + 4 * group, KT - 4)); };
-  auto copy_scales = [&](int group) {
-    const int ks = group_start(group);
+  auto copy_scales = [&](int b) {
+    const uint32_t c = 4u * (uint32_t)group_start(2 * b + ((lane & 1) ^ ((lane >> 4) & 1)));
 #pragma unroll
     for (int u = 0; u < CS; ++u)
-      lds_copy16(soff[u], wsb + (size_t)ks * 4,
-                 smem_base + kScales + (uint32_t)(group & 1) * kGroup4 + min(wave + W * u, kSUnits - 1) * 1024);
+      lds_copy16(soff[u] + c, wsb, smem_base + (uint32_t)(kScales + min(wave + W * u, kSUnits - 1) * 1024));
   };
 
   f32x4 acc[FM][FN];
@@ -386,18 +385,18 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a16_kernel(MxTileArgs a) {
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const uint32_t xrow = (uint32_t)(kX + (wm * FM * 16 + r) * 256);
   const uint32_t wfrag = (uint32_t)(kW + (wn * FN * 16 + r) * 64 + ((q ^ ((r >> 2) & 3)) * 16));
-  const uint32_t wsrow = (uint32_t)(kScales + (wn * FN * 16 + r) * 16);
+  const uint32_t wsrow = (uint32_t)(kScales + (wn * FN * 16 + r) * 32);
   const uint32_t sel = (uint32_t)(q | ((q + 4) << 8)) | 0x0C0C0000u;
 
   bf16x8 x[2][FM];                              // activation fragments of this step and the next
   u32x4 w[FN], wn_[FN];                         // codes of this stage and the next
   uint32_t sc[FN], scn[FN];                     // packed scale bytes of four stages, and the next four
   auto read_x = [&](int buf, uint32_t slot, int v, int i) {
-    x[buf][i] = *reinterpret_cast<const bf16x8*>(smem + slot + xrow + i * 4096 + (uint32_t)(((4 * q + v) ^ r) * 16));
+    x[buf][i] = *reinterpret_cast<const bf16x8*>(smem + slot + xrow + i * 4096 + (uint32_t)(((4 * q + v) ^ mx_swizzle16(r)) * 16));
   };
   auto read_w = [&](uint32_t slot, int j) { return *reinterpret_cast<const u32x4*>(smem + slot + wfrag + j * 1024); };
   auto read_scales = [&](int group, int j) {
-    return *reinterpret_cast<const u32x4*>(smem + (uint32_t)(group & 1) * kGroup4 + wsrow + j * 256);
+    return *reinterpret_cast<const u32x4*>(smem + wsrow + j * 512 + (uint32_t)(((group & 1) ^ ((r >> 3) & 1)) * 16));
   };
   auto shift_of = [&](int group) { return 8 * min(3, kt0 + 4 * group - group_start(group)); };
 
@@ -442,7 +441,8 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a16_kernel(MxTileArgs a) {
         const int tc = v == 3 ? t : (v + 1) * T + t;      // matrix instructions since the slot was free
         if (tc % kEvery == 0 && tc / kEvery <= C) {
           const int u = tc / kEvery;
-          if (u == 0) { if constexpr (J == 1) copy_scales((stage + 3) >> 2); }
+          // the last group of the scales in LDS is in registers by now
+          if (u == 0) { if (J == 1 && ((stage + 3) & 7) == 0) copy_scales((stage + 3) >> 3); }
           else copy(src, v == 3 ? slot : other, u - 1);
         }
         const int per = (kReads + T - 1) / T;

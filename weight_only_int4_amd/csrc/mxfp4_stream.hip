@@ -24,7 +24,7 @@
 // bf16 activations are loaded in whole rows (16 lanes to the 256 bytes of a slice) and
 // turned into operand order through 4 KB of LDS per wave: in operand order a load would be
 // 64 pieces of 16 bytes, four times the cache lines.  Chunk k of column c is at position k ^
-// c, so that both sides are free of bank conflicts.
+// mx_swizzle16(c), so that both sides are free of bank conflicts.
 // Loads are range-checked buffer loads: rows past M and N and blocks past K read
 // zeros and touch no memory.
 #include <algorithm>
@@ -138,12 +138,12 @@ __global__ __launch_bounds__(kMxStreamWaves * 64) void mx_stream_kernel(MxStream
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int c = 4 * v + q;
-          *reinterpret_cast<u32x4*>(turn + c * 256 + ((r ^ c) * 16)) = s.x[i][v];
+          *reinterpret_cast<u32x4*>(turn + c * 256 + ((r ^ mx_swizzle16(c)) * 16)) = s.x[i][v];
         }
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          x[i][v] = *reinterpret_cast<const bf16x8*>(turn + r * 256 + (((4 * q + v) ^ r) * 16));
+          x[i][v] = *reinterpret_cast<const bf16x8*>(turn + r * 256 + (((4 * q + v) ^ mx_swizzle16(r)) * 16));
         __builtin_amdgcn_wave_barrier();
       }
 #pragma unroll
