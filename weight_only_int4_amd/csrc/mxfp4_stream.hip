@@ -289,7 +289,8 @@ int launch_act(const MxStreamArgs& a, const MxStreamPlan& p, hipStream_t stream)
 //    CUs.  M = 16: 640 tiles 18.5 with four against 21.8 with two, 384 tiles 4.6 with two against
 //    5.3 with one, 256 tiles 5.9 with one against 6.6 with two.  From 25 rows on two (registers).
 //  * Waves: with few workgroups the waves split K four ways; many workgroups need none of it
-//    (M = 1, K = 5120, N = 17408: 10.2 with one against 11.4 with four).
+//    (K = 5120, N = 17408: M = 1 10.2 with one against 11.4 with four, M = 16 15.3 against 17.0 with
+//    two).
 //  * K is split over workgroups, with a second launch, where few tiles meet a long K: M = 37,
 //    K = 6144, N = 2048 9.1 against 10.7.
 MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N) {
@@ -309,7 +310,7 @@ MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N) {
     p.splits = 4;
   }
   const long long wgs = (tiles + p.cols - 1) / p.cols * p.splits;
-  p.waves = wgs <= 512 ? 4 : wgs <= 1280 && M <= 24 ? 2 : 1;
+  p.waves = wgs <= 512 ? 4 : wgs <= 1280 && M <= 8 ? 2 : 1;
   while (p.waves > 1 && 2 * p.waves * p.splits > steps) p.waves /= 2;   // two steps a wave at least
   return p;
 }
