@@ -423,6 +423,7 @@ int awq_search_lookahead(const uint16_t* X, int B, int L, int hidden, int n_q, i
  *     8 i + j: bit 3 the sign, bits 0-2 the magnitude 0, 0.5, 1, 1.5, 2, 3, 4, 6.
  *   - The value of an element is its magnitude with its sign times its block's scale.
  *   - A call with N == 0 (or M == 0) succeeds and enqueues nothing.
+ *   - Outputs must not overlap inputs or the workspace.
  *
  * mxfp4_quantize -- v = W diag(s) to MXFP4, weights and activations alike.  Per block,
  *   with v = W[n][k] s[k] in fp32 (s == NULL: v = W[n][k]) and A = max |v|:
@@ -452,7 +453,8 @@ int mxfp4_dequantize(const uint32_t* codes, const uint8_t* scales, int N, int K,
  *   by (M, K, N), rounded to nearest even at the store.  A weight block with byte 255
  *   makes its output channel NaN, an activation block with byte 255 its row;
  *   mxfp4_a16_gemm takes weights as the bf16 values of mxfp4_dequantize.
- *   W4_ERR_SHAPE (from the size query too) when K > 2,097,152.
+ *   W4_ERR_SHAPE (from the size query too) when K > 2,097,152 or M or N > 2,147,482,624;
+ *   from the call when the output needs more than 2^31 - 1 workgroups.
  *   Size query and workspace as in w4a16_gemv; the size depends only on (M, K, N).
  */
 int mxfp4_a16_gemm(const uint16_t* X, int M, int K, int N, const uint32_t* qweight, const uint8_t* scales,

@@ -189,6 +189,97 @@ def test_product_model_sizes(M, K, N, act):
     assert bool(((Y - ref).abs() <= bound).all())
 
 
+# Shapes of the tiled form: ragged in every direction, K that ends inside a stage and inside four
+# stages, scale rows that need padding, K split over workgroups, one and several rounds.
+TILED = [(520, 2080, 1001), (700, 1568, 1003), (257, 4160, 1000), (40, 17408, 1500), (300, 17440, 255), (513, 2016, 2050),
+         (1030, 1024, 1026), (2049, 640, 1030), (130, 8192, 1001), (4100, 512, 513), (48, 5120, 5119), (2047, 2048, 3000)]
+
+
+def _gpu_reference(X, W):
+    """product_bound on the GPU, for shapes whose fp64 product would take long on the host."""
+    ref, mag = X @ W.T, X.abs() @ W.abs().T
+    acc = X.shape[1] * 2.0 ** -23 * mag
+    return ref, acc + 2.0 ** -8 * (ref.abs() + acc) + 2.0 ** -134
+
+
+def _random_packed(gen, rows, K):
+    qw = torch.randint(-2 ** 31, 2 ** 31 - 1, (rows, K // 8), generator=gen, device="cuda", dtype=torch.int32)
+    sw = torch.randint(112, 130, (rows, K // 32), generator=gen, device="cuda", dtype=torch.uint8)
+    return qw, sw, w4.mxfp4_dequantize(qw, sw).double()
+
+
+@pytest.mark.parametrize("act", [16, 4])
+@pytest.mark.parametrize("M,K,N", TILED)
+def test_product_tiled(M, K, N, act):
+    say("mx product tiled", M, K, N, act)
+    gen = torch.Generator(device="cuda").manual_seed(M + 3 * K + 7 * N)
+    qw, sw, W = _random_packed(gen, N, K)
+    if act == 16:
+        acts = (torch.randn(M, K, generator=gen, device="cuda").bfloat16(),)
+        X = acts[0].double()
+    else:
+        *acts, X = _random_packed(gen, M, K)
+    buf = torch.full((M * N + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
+    Y = buf[64:64 + M * N].view(M, N)
+    _product(act, acts, qw, sw, Y=Y)
+    ref, bound = _gpu_reference(X, W)
+    assert bool(((Y.double() - ref).abs() <= bound).all())
+    assert bool((buf[:64] == 7.0).all()) and bool((buf[64 + M * N:] == 7.0).all())
+    again = _product(act, acts, qw, sw, workspace=torch.full((512 << 20,), 0xFF, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(Y, again)
+
+
+@pytest.mark.parametrize("act", [16, 4])
+@pytest.mark.parametrize("M,K,N", [(520, 2080, 1001), (257, 4160, 1000), (40, 17408, 1500), (2047, 2048, 3000)])
+def test_product_tiled_special_values(M, K, N, act):
+    """NaN scale bytes and non-finite activations in the tiled form, in the first and the last block
+    of K: one channel or one row each, and nothing else."""
+    say("mx product tiled special", M, K, N, act)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    qw, sw, _ = _random_packed(gen, N, K)
+    sw[5, 0] = 255
+    sw[N - 1, K // 32 - 1] = 255
+    if act == 16:
+        acts = (torch.randn(M, K, generator=gen, device="cuda").bfloat16(),)
+        acts[0][3, 1] = float("nan")
+        acts[0][M - 1, K - 1] = float("inf")
+    else:
+        *acts, _ = _random_packed(gen, M, K)
+        acts[1][3, 0] = 255
+        acts[1][M - 1, K // 32 - 1] = 255
+    Y = _product(act, acts, qw, sw).float()
+    assert bool(Y[:, [5, N - 1]].isnan().all())
+    rest = torch.ones(M, N, dtype=torch.bool, device="cuda")
+    rest[:, [5, N - 1]] = False
+    rest[[3, M - 1]] = False
+    assert bool(Y[rest].isfinite().all())
+    if act == 4:
+        assert bool(Y[[3, M - 1]].isnan().all())
+    else:
+        assert bool(Y[3].isnan().all())
+        last = qw[:, -1] >> 28                              # the last channel's codes: +-inf, or NaN where zero
+        want_nan = (last & 7) == 0
+        want_nan[[5, N - 1]] = True
+        assert bool((Y[M - 1].isnan() == want_nan).all())
+        assert bool((~Y[M - 1].isfinite()).all())
+
+
+@pytest.mark.parametrize("act", [16, 4])
+def test_product_many_rows_one_channel(act):
+    """More row groups than a grid dimension other than the first may have."""
+    M, K, N = 4_300_000, 32, 1
+    say("mx product many rows", M, act)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    qw, sw, W = _random_packed(gen, N, K)
+    if act == 16:
+        acts = (torch.randn(M, K, generator=gen, device="cuda").bfloat16(),)
+        X = acts[0].double()
+    else:
+        *acts, X = _random_packed(gen, M, K)
+    ref, bound = _gpu_reference(X, W)
+    assert bool(((_product(act, acts, qw, sw).double() - ref).abs() <= bound).all())
+
+
 @pytest.mark.parametrize("act", [16, 4])
 @pytest.mark.parametrize("M", [1, 3, 6, 16, 40, 70, 300])
 def test_product_nan_blocks_stay_in_their_channel(M, act):

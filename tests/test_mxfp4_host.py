@@ -136,7 +136,8 @@ def _gemm_calls(lib):
 def test_gemm_refusals(lib):
     sz = ctypes.c_size_t(0)
     for name, f in _gemm_calls(lib):
-        for M, K, N in ((-1, 64, 8), (1, 0, 8), (1, 33, 8), (1, 64, -1), (1, (1 << 21) + 32, 8)):
+        for M, K, N in ((-1, 64, 8), (1, 0, 8), (1, 33, 8), (1, 64, -1), (1, (1 << 21) + 32, 8), (2 ** 31 - 1, 32, 1),
+                        (1, 32, 2 ** 31 - 1)):
             assert f(M, K, N) == -2, (name, M, K, N)
             assert f(M, K, N, sz=ctypes.byref(sz)) == -2
         for kw in (dict(x=None), dict(w=None), dict(s=None), dict(y=None)) + ((dict(xs=None),) if name == "a4" else ()):

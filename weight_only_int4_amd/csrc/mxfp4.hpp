@@ -16,6 +16,8 @@ constexpr int kMxBlock = 32;                 // channels per shared scale
 // Longest K of the products: a tile of up to 256 rows of 2-byte activations stays
 // below 2^31 bytes, the range of a buffer descriptor's 32-bit offsets used here.
 constexpr int kMxMaxK = 1 << 21;
+// Most rows and channels of the products: a tile's last row index is still an int.
+constexpr int kMxMaxRows = 0x7FFFFFFF - 1023;
 
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
 typedef int i32x8 __attribute__((ext_vector_type(8)));

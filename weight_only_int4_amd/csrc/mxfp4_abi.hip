@@ -13,7 +13,7 @@ int check_matrix(int N, int K) { return N < 0 || K <= 0 || K % kMxBlock ? W4_ERR
 // Shapes, size query, workspace, pointers: the order every workspace-taking call uses.
 int run_gemm(const MxGemmArgs& g, size_t* workspace_bytes, void* stream) {
   if (int st = check_matrix(g.N, g.K)) return st;
-  if (g.M < 0 || g.K > kMxMaxK) return W4_ERR_SHAPE;
+  if (g.M < 0 || g.M > kMxMaxRows || g.N > kMxMaxRows || g.K > kMxMaxK) return W4_ERR_SHAPE;
   const size_t need = mxfp4_gemm_workspace_bytes(g.act_bits, g.M, g.K, g.N);
   if (!g.workspace && workspace_bytes) {
     *workspace_bytes = need;

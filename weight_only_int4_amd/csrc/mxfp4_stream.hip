@@ -26,7 +26,8 @@
 // 64 pieces of 16 bytes, four times the cache lines.  Chunk k of column c is at position k ^
 // mx_swizzle16(c), so that both sides are free of bank conflicts.
 // Loads are range-checked buffer loads: rows past M and N and blocks past K read
-// zeros and touch no memory.
+// zeros and touch no memory.  The whole offset is in the checked lane offset: the scalar
+// one of these instructions is added after the check.
 #include <algorithm>
 
 #include "mxfp4.hpp"
@@ -44,6 +45,7 @@ struct MxStreamArgs {
   uint16_t* Y;
   float* partial;         // [splits][M][N] when K is split over blockIdx.z, else NULL
   int steps;              // steps of one split
+  int col_groups;         // workgroups side by side along N; blockIdx.x counts them row group by row group
 };
 
 // Sum over the SL neighbouring lanes of a slice group (1, 2 or 4 lanes).
@@ -69,7 +71,8 @@ __global__ __launch_bounds__(kMxStreamWaves * 64) void mx_stream_kernel(MxStream
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   const int r = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * kCh * CB, m0 = blockIdx.y * kCh * RB;
+  const int n0 = (int)(blockIdx.x % (uint32_t)a.col_groups) * kCh * CB;
+  const int m0 = (int)(blockIdx.x / (uint32_t)a.col_groups) * kCh * RB;
   const int KB = a.K / kMxBlock;
   const int nrows = min(kCh * CB, a.N - n0), mrows = min(kCh * RB, a.M - m0);
   const auto rw = make_rsrc(a.qweight + (size_t)n0 * (a.K / 8), (uint32_t)nrows * (uint32_t)(a.K / 2));
@@ -106,20 +109,20 @@ __global__ __launch_bounds__(kMxStreamWaves * 64) void mx_stream_kernel(MxStream
     const uint32_t wk = kq < left ? wo + 16u * (kb + kq) : kOob, sk = kq < left ? so + kb + kq : kOob;
 #pragma unroll
     for (int j = 0; j < CB; ++j) {
-      s.w[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wk, (int)(j * wstep), 0));
-      s.ws[j] = __builtin_amdgcn_raw_buffer_load_b8(rs, sk, (int)(j * sstep), 0);
+      s.w[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wk + j * wstep, 0, 0));
+      s.ws[j] = __builtin_amdgcn_raw_buffer_load_b8(rs, sk + j * sstep, 0, 0);
     }
 #pragma unroll
     for (int v = 0; v < XV; ++v) {
       const uint32_t o = xk[v] < left ? xo[v] + (ACT == 16 ? 64u : 16u) * kb : kOob;
 #pragma unroll
       for (int i = 0; i < RB; ++i)
-        s.x[i][v] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, o, (int)(i * xtile), 0));
+        s.x[i][v] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, o + i * xtile, 0, 0));
     }
     if constexpr (ACT == 4) {
 #pragma unroll
       for (int i = 0; i < RB; ++i)
-        s.xs[i] = __builtin_amdgcn_raw_buffer_load_b8(rxs, sk, (int)(i * sstep), 0);
+        s.xs[i] = __builtin_amdgcn_raw_buffer_load_b8(rxs, sk + i * sstep, 0, 0);
     }
   };
 
@@ -237,10 +240,11 @@ int launch_stream(const MxStreamArgs& base, int waves, int splits, hipStream_t s
   const int nc = 16 / SL * CB;
   const int mr = 16 / SL * RB;
   const long long gx = (a.N + nc - 1LL) / nc, gy = (a.M + mr - 1LL) / mr;
-  if (gy > 65535) return W4_ERR_SHAPE;
+  if (gx * gy > 0x7FFFFFFFLL) return W4_ERR_SHAPE;
+  a.col_groups = (int)gx;
   const size_t lds =
       std::max<size_t>((size_t)waves * (16 / SL) * (nc + 4) * sizeof(float), ACT == 16 ? waves * kMxTurn : 0);
-  hipLaunchKernelGGL((mx_stream_kernel<ACT, SL, RB, CB>), dim3((unsigned)gx, (unsigned)gy, (unsigned)splits),
+  hipLaunchKernelGGL((mx_stream_kernel<ACT, SL, RB, CB>), dim3((unsigned)(gx * gy), 1, (unsigned)splits),
                      dim3(waves * 64), lds, stream, a);
   W4_CHECK_LAUNCH();
   return W4_OK;
@@ -317,7 +321,7 @@ MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N) {
 
 int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t stream) {
   MxStreamArgs a{g.X, g.Xq, g.xscales, g.M, g.K, g.N, g.qweight, g.scales, g.Y,
-                 p.splits > 1 ? static_cast<float*>(g.workspace) : nullptr, 0};
+                 p.splits > 1 ? static_cast<float*>(g.workspace) : nullptr, 0, 0};
   const int st = g.act_bits == 16 ? launch_act<16>(a, p, stream) : launch_act<4>(a, p, stream);
   if (st || p.splits == 1) return st;
   const size_t MN = (size_t)g.M * g.N;
@@ -331,11 +335,11 @@ int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t str
 // Where scale rows have to be padded first, by another launch, it has to be worth that
 // (4-bit, M = 333, K = 1056, N = 2047: 7.8 here against 9.5).
 bool mxfp4_use_tile(int act_bits, int M, int K, int N) {
-  const long long NK = (long long)N * K, MNK = M * NK;
-  if (act_bits == 16) return M > 32 && MNK >= 1000000000LL;
+  const double NK = (double)N * K, MNK = M * NK;
+  if (act_bits == 16) return M > 32 && MNK >= 1e9;
   const int KB = K / kMxBlock;
-  if (KB % 4 != 0 || KB < 16) return MNK >= 2000000000LL;
-  return M > (NK >= (8LL << 20) ? 16 : 32);
+  if (KB % 4 != 0 || KB < 16) return MNK >= 2e9;
+  return M > (NK >= 8e6 ? 16 : 32);
 }
 
 size_t mxfp4_gemm_workspace_bytes(int act_bits, int M, int K, int N) {
