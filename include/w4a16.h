@@ -432,6 +432,7 @@ int awq_search_lookahead(const uint16_t* X, int B, int L, int hidden, int n_q, i
  *            code, saturating at 6; the sign of v is kept, also that of zero.
  *   A block with an infinite or NaN v gets byte 255 and codes 0.  Bit-identical to
  *   this definition for every input.
+ *   W4_ERR_SHAPE when N K > 2^35 - 2,048 (here and in mxfp4_dequantize).
  *   W [N][K] bf16.  s [K] fp32 or NULL.  codes [N][K/8], scales [N][K/32] out.
  */
 int mxfp4_quantize(const uint16_t* W, int N, int K, const float* s, uint32_t* codes, uint8_t* scales,
@@ -453,8 +454,8 @@ int mxfp4_dequantize(const uint32_t* codes, const uint8_t* scales, int N, int K,
  *   by (M, K, N), rounded to nearest even at the store.  A weight block with byte 255
  *   makes its output channel NaN, an activation block with byte 255 its row;
  *   mxfp4_a16_gemm takes weights as the bf16 values of mxfp4_dequantize.
- *   W4_ERR_SHAPE (from the size query too) when K > 2,097,152 or M or N > 2,147,482,624;
- *   from the call when the output needs more than 2^31 - 1 workgroups.
+ *   W4_ERR_SHAPE (from the size query too) when K > 2,097,152 or M or N > 2,147,482,624,
+ *   or the shape needs 2^32 or more threads.
  *   Size query and workspace as in w4a16_gemv; the size depends only on (M, K, N).
  */
 int mxfp4_a16_gemm(const uint16_t* X, int M, int K, int N, const uint32_t* qweight, const uint8_t* scales,

@@ -104,6 +104,7 @@ def test_quantize_refusals(lib):
     for K in (0, -32, 31, 48):
         assert f(A, 4, K, None, A, A, None) == -2
     assert f(A, -1, 64, None, A, A, None) == -2
+    assert f(A, 2 ** 31 - 1, 32, None, A, A, None) == -2
     assert f(None, 4, 64, None, A, A, None) == -1
     assert f(A, 4, 64, None, None, A, None) == -1
     assert f(A, 4, 64, None, A, None, None) == -1
@@ -118,6 +119,7 @@ def test_dequantize_refusals(lib):
     f = lib.mxfp4_dequantize
     assert f(A, A, 4, 40, A, None) == -2
     assert f(A, A, -4, 64, A, None) == -2
+    assert f(A, A, 2 ** 31 - 1, 32, A, None) == -2
     for i in (0, 1, 4):
         args = [A, A, 4, 64, A, None]
         args[i] = None
@@ -137,7 +139,7 @@ def test_gemm_refusals(lib):
     sz = ctypes.c_size_t(0)
     for name, f in _gemm_calls(lib):
         for M, K, N in ((-1, 64, 8), (1, 0, 8), (1, 33, 8), (1, 64, -1), (1, (1 << 21) + 32, 8), (2 ** 31 - 1, 32, 1),
-                        (1, 32, 2 ** 31 - 1)):
+                        (1, 32, 2 ** 31 - 1), (1 << 30, 32, 1 << 30), (1 << 20, 2080, 1 << 29)):
             assert f(M, K, N) == -2, (name, M, K, N)
             assert f(M, K, N, sz=ctypes.byref(sz)) == -2
         for kw in (dict(x=None), dict(w=None), dict(s=None), dict(y=None)) + ((dict(xs=None),) if name == "a4" else ()):

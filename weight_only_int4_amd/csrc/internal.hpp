@@ -159,16 +159,23 @@ struct MxStreamPlan {
 };
 struct MxTilePlan {
   int tile, splits, stages;                // tile shape, split of K, 128-channel stages of a split
-  double us;                               // estimated time
 };
 MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N);
 MxTilePlan plan_mx_tile(int act_bits, int M, int K, int N);
 bool mxfp4_use_tile(int act_bits, int M, int K, int N);
+bool mx_stream_fits(const MxStreamPlan& p, int M, int N);                      // the grid is within limits
+bool mx_tile_fits(const MxTilePlan& p, int act_bits, int M, int K, int N);
 size_t mx_tile_workspace_bytes(const MxTilePlan& p, int act_bits, int M, int K, int N);
 int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t stream);
 int launch_mx_tile(const MxTilePlan& p, const MxGemmArgs& g, hipStream_t stream);
-size_t mxfp4_gemm_workspace_bytes(int act_bits, int M, int K, int N);
-int launch_mxfp4_gemm(const MxGemmArgs& g, hipStream_t stream);
+struct MxPlan {
+  bool use_tile, fits;
+  MxStreamPlan stream;
+  MxTilePlan tile;
+  size_t workspace;
+};
+MxPlan plan_mxfp4_gemm(int act_bits, int M, int K, int N);
+int launch_mxfp4_gemm(const MxPlan& p, const MxGemmArgs& g, hipStream_t stream);
 
 // m_k = mean_t |X[t][k]| in fp64, fixed summation order.
 // m must hold (1 + ceil(T / 64)) * K doubles: m[0..K) is the result, the rest

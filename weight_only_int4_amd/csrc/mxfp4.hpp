@@ -18,6 +18,10 @@ constexpr int kMxBlock = 32;                 // channels per shared scale
 constexpr int kMxMaxK = 1 << 21;
 // Most rows and channels of the products: a tile's last row index is still an int.
 constexpr int kMxMaxRows = 0x7FFFFFFF - 1023;
+// Most threads along one dimension of a grid (its size in work items is a 32-bit field).
+constexpr long long kMaxGridThreads = 0xFFFFFFFFLL;
+// Most elements of one conversion: a thread takes eight.
+constexpr long long kMxMaxElements = (kMaxGridThreads - 255) / 256 * 256 * 8;
 
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
 typedef int i32x8 __attribute__((ext_vector_type(8)));

@@ -8,13 +8,22 @@ namespace {
 
 inline bool misaligned(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
-int check_matrix(int N, int K) { return N < 0 || K <= 0 || K % kMxBlock ? W4_ERR_SHAPE : W4_OK; }
+int check_matrix(int N, int K) {
+  return N < 0 || K <= 0 || K % kMxBlock ? W4_ERR_SHAPE : W4_OK;
+}
+
+int check_conversion(int N, int K) {
+  if (int st = check_matrix(N, K)) return st;
+  return (long long)N * K > kMxMaxElements ? W4_ERR_SHAPE : W4_OK;
+}
 
 // Shapes, size query, workspace, pointers: the order every workspace-taking call uses.
 int run_gemm(const MxGemmArgs& g, size_t* workspace_bytes, void* stream) {
   if (int st = check_matrix(g.N, g.K)) return st;
   if (g.M < 0 || g.M > kMxMaxRows || g.N > kMxMaxRows || g.K > kMxMaxK) return W4_ERR_SHAPE;
-  const size_t need = mxfp4_gemm_workspace_bytes(g.act_bits, g.M, g.K, g.N);
+  const MxPlan plan = plan_mxfp4_gemm(g.act_bits, g.M, g.K, g.N);
+  if (!plan.fits) return W4_ERR_SHAPE;
+  const size_t need = plan.workspace;
   if (!g.workspace && workspace_bytes) {
     *workspace_bytes = need;
     return W4_OK;
@@ -26,7 +35,7 @@ int run_gemm(const MxGemmArgs& g, size_t* workspace_bytes, void* stream) {
   if (misaligned(g.X) || misaligned(g.Xq) || misaligned(g.xscales) || misaligned(g.qweight) || misaligned(g.scales) ||
       misaligned(g.Y) || misaligned(g.workspace))
     return W4_ERR_ALIGN;
-  return launch_mxfp4_gemm(g, static_cast<hipStream_t>(stream));
+  return launch_mxfp4_gemm(plan, g, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace
@@ -34,7 +43,7 @@ int run_gemm(const MxGemmArgs& g, size_t* workspace_bytes, void* stream) {
 extern "C" {
 
 int mxfp4_quantize(const uint16_t* W, int N, int K, const float* s, uint32_t* codes, uint8_t* scales, void* stream) {
-  if (int st = check_matrix(N, K)) return st;
+  if (int st = check_conversion(N, K)) return st;
   if (N == 0) return W4_OK;
   if (!W || !codes || !scales) return W4_ERR_NULL;
   if (misaligned(W) || misaligned(s) || misaligned(codes) || misaligned(scales)) return W4_ERR_ALIGN;
@@ -42,7 +51,7 @@ int mxfp4_quantize(const uint16_t* W, int N, int K, const float* s, uint32_t* co
 }
 
 int mxfp4_dequantize(const uint32_t* codes, const uint8_t* scales, int N, int K, uint16_t* W, void* stream) {
-  if (int st = check_matrix(N, K)) return st;
+  if (int st = check_conversion(N, K)) return st;
   if (N == 0) return W4_OK;
   if (!codes || !scales || !W) return W4_ERR_NULL;
   if (misaligned(codes) || misaligned(scales) || misaligned(W)) return W4_ERR_ALIGN;

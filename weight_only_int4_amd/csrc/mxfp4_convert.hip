@@ -69,8 +69,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* code
 int launch_mxfp4_quantize(const uint16_t* W, int N, int K, const float* s, uint32_t* codes, uint8_t* scales,
                           hipStream_t stream) {
   const size_t chunks = (size_t)N * (K / 8);
-  const size_t blocks = (chunks + 255) / 256;
-  if (blocks > 0x7FFFFFFFu) return W4_ERR_SHAPE;
+  const size_t blocks = (chunks + 255) / 256;   // kMxMaxElements bounds it
   const uint4* w = reinterpret_cast<const uint4*>(W);
   if (s)
     hipLaunchKernelGGL(mx_quantize_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, stream, w, chunks, K / 8,
@@ -86,7 +85,6 @@ int launch_mxfp4_dequantize(const uint32_t* codes, const uint8_t* scales, int N,
                             hipStream_t stream) {
   const size_t chunks = (size_t)N * (K / 8);
   const size_t blocks = (chunks + 255) / 256;
-  if (blocks > 0x7FFFFFFFu) return W4_ERR_SHAPE;
   hipLaunchKernelGGL(mx_dequantize_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, codes, scales, chunks,
                      reinterpret_cast<uint4*>(W));
   W4_CHECK_LAUNCH();

@@ -48,6 +48,8 @@ double tile_cost(const MxTile& t, long long wgs, int stages) {
   return us;
 }
 
+long long workgroups(const MxTile& t, int M, int N) { return ((M + t.bm - 1LL) / t.bm) * ((N + t.bn - 1LL) / t.bn); }
+
 int padded_scale_row(int KB) { return KB % 4 == 0 && KB >= 16 ? 0 : std::max(16, (KB + 3) / 4 * 4); }
 
 }  // namespace
@@ -59,7 +61,7 @@ MxTilePlan plan_mx_tile(int act_bits, int M, int K, int N) {
   MxTilePlan best{};
   double best_us = DBL_MAX;
   for (int i = 0; i < count; ++i) {
-    const long long n = ((M + tiles[i].bm - 1LL) / tiles[i].bm) * ((N + tiles[i].bn - 1LL) / tiles[i].bn);
+    const long long n = workgroups(tiles[i], M, N);
     for (int splits = 1; splits <= 16; splits *= 2) {
       const int per = (KT + splits - 1) / splits, stages = splits == 1 ? KT : (per + 3) / 4 * 4;
       const int actual = (KT + stages - 1) / stages;
@@ -69,7 +71,7 @@ MxTilePlan plan_mx_tile(int act_bits, int M, int K, int N) {
       if (actual > 1) us += 3.0 + 8.0 * actual * M * N / 3.0e6;
       if (us < best_us) {
         best_us = us;
-        best = MxTilePlan{i, actual, splits == 1 ? (KT + 3) / 4 * 4 : stages, us};
+        best = MxTilePlan{i, actual, splits == 1 ? (KT + 3) / 4 * 4 : stages};
       }
     }
   }
@@ -95,6 +97,12 @@ size_t mx_tile_workspace_bytes(const MxTilePlan& p, int act_bits, int M, int K, 
   return tile_layout(p, act_bits, M, K, N).total;
 }
 
+bool mx_tile_fits(const MxTilePlan& p, int act_bits, int M, int K, int N) {
+  const MxTile& t = act_bits == 4 ? kTiles4[p.tile] : kTiles16[p.tile];
+  const long long padded = (N + (act_bits == 4 ? (long long)M : 0)) * padded_scale_row(K / kMxBlock);
+  return workgroups(t, M, N) * 256 <= kMaxGridThreads && (padded + 255) / 256 * 256 <= kMaxGridThreads;
+}
+
 int launch_mx_tile(const MxTilePlan& p, const MxGemmArgs& g, hipStream_t stream) {
   const int KB = g.K / kMxBlock, ss = padded_scale_row(KB);
   const MxTileLayout l = tile_layout(p, g.act_bits, g.M, g.K, g.N);
@@ -113,18 +121,14 @@ int launch_mx_tile(const MxTilePlan& p, const MxGemmArgs& g, hipStream_t stream)
   a.partial = p.splits > 1 ? reinterpret_cast<float*>(ws + l.partial) : nullptr;
   if (ss) {
     const int rows = g.act_bits == 4 ? g.M : 0;
-    const size_t blocks = ((size_t)(g.N + (long long)rows) * ss + 255) / 256;
-    if (blocks > 0x7FFFFFFFu) return W4_ERR_SHAPE;
+    const size_t blocks = ((size_t)(g.N + (long long)rows) * ss + 255) / 256;   // mx_tile_fits
     hipLaunchKernelGGL(mx_pad_scales_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, g.scales, g.N, g.xscales, rows,
                        KB, ws + l.w, ws + l.x, ss);
     a.ws = ws + l.w;
     a.xs = ws + l.x;
     a.ss = ss;
   }
-  const MxTile& t = g.act_bits == 4 ? kTiles4[p.tile] : kTiles16[p.tile];
-  const long long n = ((g.M + t.bm - 1LL) / t.bm) * ((g.N + t.bn - 1LL) / t.bn);
-  if (n > 0x7FFFFFFFLL) return W4_ERR_SHAPE;
-  const dim3 grid((unsigned)n, (unsigned)p.splits), block(256);
+  const dim3 grid((unsigned)workgroups(g.act_bits == 4 ? kTiles4[p.tile] : kTiles16[p.tile], g.M, g.N), (unsigned)p.splits), block(256);
   if (g.act_bits == 4) {
     switch (p.tile) {
       case 0: hipLaunchKernelGGL((mx_tile_a4_kernel<256, 256>), grid, block, 0, stream, a); break;

@@ -237,10 +237,8 @@ int launch_stream(const MxStreamArgs& base, int waves, int splits, hipStream_t s
   MxStreamArgs a = base;
   const int steps = (a.K / kMxBlock + 4 * SL - 1) / (4 * SL);
   a.steps = (steps + splits - 1) / splits;
-  const int nc = 16 / SL * CB;
-  const int mr = 16 / SL * RB;
-  const long long gx = (a.N + nc - 1LL) / nc, gy = (a.M + mr - 1LL) / mr;
-  if (gx * gy > 0x7FFFFFFFLL) return W4_ERR_SHAPE;
+  const int nc = 16 / SL * CB, mr = 16 / SL * RB;
+  const long long gx = (a.N + nc - 1LL) / nc, gy = (a.M + mr - 1LL) / mr;   // mx_stream_fits
   a.col_groups = (int)gx;
   const size_t lds =
       std::max<size_t>((size_t)waves * (16 / SL) * (nc + 4) * sizeof(float), ACT == 16 ? waves * kMxTurn : 0);
@@ -249,10 +247,6 @@ int launch_stream(const MxStreamArgs& base, int waves, int splits, hipStream_t s
   W4_CHECK_LAUNCH();
   return W4_OK;
 }
-
-}  // namespace
-
-namespace {
 
 template <int ACT, int SL, int RB>
 int launch_cols(const MxStreamArgs& a, const MxStreamPlan& p, hipStream_t stream) {
@@ -319,6 +313,11 @@ MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N) {
   return p;
 }
 
+bool mx_stream_fits(const MxStreamPlan& p, int M, int N) {
+  const int nc = 16 / p.slices * p.cols, mr = 16 / p.slices * p.rows;
+  return (N + nc - 1LL) / nc * ((M + mr - 1LL) / mr) * p.waves * 64 <= kMaxGridThreads;
+}
+
 int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t stream) {
   MxStreamArgs a{g.X, g.Xq, g.xscales, g.M, g.K, g.N, g.qweight, g.scales, g.Y,
                  p.splits > 1 ? static_cast<float*>(g.workspace) : nullptr, 0, 0};
@@ -342,16 +341,25 @@ bool mxfp4_use_tile(int act_bits, int M, int K, int N) {
   return M > (NK >= 8e6 ? 16 : 32);
 }
 
-size_t mxfp4_gemm_workspace_bytes(int act_bits, int M, int K, int N) {
-  if (M == 0 || N == 0) return 0;
-  if (mxfp4_use_tile(act_bits, M, K, N)) return mx_tile_workspace_bytes(plan_mx_tile(act_bits, M, K, N), act_bits, M, K, N);
-  const MxStreamPlan p = plan_mx_stream(act_bits, M, K, N);
-  return p.splits > 1 ? (size_t)p.splits * M * N * sizeof(float) : 0;
+MxPlan plan_mxfp4_gemm(int act_bits, int M, int K, int N) {
+  MxPlan p{};
+  p.fits = true;
+  if (M == 0 || N == 0) return p;
+  p.use_tile = mxfp4_use_tile(act_bits, M, K, N);
+  if (p.use_tile) {
+    p.tile = plan_mx_tile(act_bits, M, K, N);
+    p.fits = mx_tile_fits(p.tile, act_bits, M, K, N);
+    p.workspace = mx_tile_workspace_bytes(p.tile, act_bits, M, K, N);
+  } else {
+    p.stream = plan_mx_stream(act_bits, M, K, N);
+    p.fits = mx_stream_fits(p.stream, M, N);
+    p.workspace = p.stream.splits > 1 ? (size_t)p.stream.splits * M * N * sizeof(float) : 0;
+  }
+  return p;
 }
 
-int launch_mxfp4_gemm(const MxGemmArgs& g, hipStream_t stream) {
-  if (mxfp4_use_tile(g.act_bits, g.M, g.K, g.N)) return launch_mx_tile(plan_mx_tile(g.act_bits, g.M, g.K, g.N), g, stream);
-  return launch_mx_stream(plan_mx_stream(g.act_bits, g.M, g.K, g.N), g, stream);
+int launch_mxfp4_gemm(const MxPlan& p, const MxGemmArgs& g, hipStream_t stream) {
+  return p.use_tile ? launch_mx_tile(p.tile, g, stream) : launch_mx_stream(p.stream, g, stream);
 }
 
 }  // namespace w4
