@@ -67,13 +67,16 @@ __device__ __forceinline__ uint32_t pack_bytes(u32x4 d, uint32_t sel) {
 template <int FN>
 constexpr int kMxStage = 16 * (FN * 32 + 16);
 
-// Rows of P-element pieces; P divides N, so pieces are whole and aligned.
-template <int FM, int FN, int P>
+// Where N is not a multiple of eight (WHOLE false) the pieces are not aligned, and the last one
+// of a row goes element by element.  (Aligned pieces of one element instead: M = 2047, K = 1536, N = 17401 took
+// 83 us against 48.)
+template <int FM, int FN, bool WHOLE>
 __device__ __forceinline__ void mx_store_rows(const MxTileArgs& a, const f32x4 (&acc)[FM][FN], int m1, int n1,
                                               unsigned char* stage) {
   typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-  typedef uint16_t piece __attribute__((ext_vector_type(P)));
-  constexpr int kRow = FN * 32 + 16, kPieces = FN * 16 / P;
+  typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+  typedef u16x8 u16x8_unaligned __attribute__((aligned(2)));
+  constexpr int kRow = FN * 32 + 16, kPieces = FN * 2;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -83,12 +86,22 @@ __device__ __forceinline__ void mx_store_rows(const MxTileArgs& a, const f32x4 (
       *reinterpret_cast<bf16x4*>(stage + r * kRow + j * 32 + q * 8) = b;
     }
     __builtin_amdgcn_wave_barrier();            // LDS operations of one wave complete in order
-#pragma unroll 4
+#pragma unroll
     for (int p = lane; p < 16 * kPieces; p += 64) {
       const int row = p / kPieces, c = p % kPieces;
-      const int m = m1 + 16 * i + row, n = n1 + P * c;
-      if (m < a.M && n < a.N)
-        *reinterpret_cast<piece*>(a.Y + (size_t)m * a.N + n) = *reinterpret_cast<const piece*>(stage + row * kRow + c * (2 * P));
+      const int m = m1 + 16 * i + row, n = n1 + 8 * c;
+      if (m >= a.M || n >= a.N) continue;
+      uint16_t* y = a.Y + (size_t)m * a.N + n;
+      const u16x8 v = *reinterpret_cast<const u16x8*>(stage + row * kRow + c * 16);
+      if (WHOLE) {
+        *reinterpret_cast<u16x8*>(y) = v;
+      } else if (n + 8 <= a.N) {
+        *reinterpret_cast<u16x8_unaligned*>(y) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+          if (n + e < a.N) y[e] = v[e];
+      }
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -98,9 +111,8 @@ template <int FM, int FN>
 __device__ __forceinline__ void mx_store_tile(const MxTileArgs& a, const f32x4 (&acc)[FM][FN], int m1, int n1,
                                               unsigned char* stage) {
   if (!a.partial) {
-    if ((a.N & 7) == 0) mx_store_rows<FM, FN, 8>(a, acc, m1, n1, stage);
-    else if ((a.N & 1) == 0) mx_store_rows<FM, FN, 2>(a, acc, m1, n1, stage);
-    else mx_store_rows<FM, FN, 1>(a, acc, m1, n1, stage);
+    if ((a.N & 7) == 0) mx_store_rows<FM, FN, true>(a, acc, m1, n1, stage);
+    else mx_store_rows<FM, FN, false>(a, acc, m1, n1, stage);
     return;
   }
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;

@@ -214,19 +214,24 @@ __global__ __launch_bounds__(kMxStreamWaves * 64) void mx_stream_kernel(MxStream
       const int m = m0 + kCh * i + row, n = n0 + c;
       if (m >= a.M) continue;
       const size_t at = (size_t)m * a.N + n;
+      const bool whole = n + 4 <= a.N;           // four outputs at once, aligned to one
       if (a.partial) {
+        typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
         float* p = a.partial + (size_t)blockIdx.z * a.M * a.N + at;
+        if (whole) *reinterpret_cast<f32x4_any*>(p) = f32x4_any{sum[0], sum[1], sum[2], sum[3]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < a.N) p[e] = sum[e];
-      } else if ((a.N & 3) == 0) {             // four whole, aligned outputs
-        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-        if (n < a.N)
-          *reinterpret_cast<bf16x4*>(a.Y + at) = bf16x4{(__bf16)sum[0], (__bf16)sum[1], (__bf16)sum[2], (__bf16)sum[3]};
+        for (int e = 0; e < 3; ++e)
+          if (!whole && n + e < a.N) p[e] = sum[e];
       } else {
+        typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+        typedef u16x4 u16x4_any __attribute__((aligned(2)));
+        u16x4 y;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < a.N) a.Y[at + e] = __builtin_bit_cast(uint16_t, (__bf16)sum[e]);
+        for (int e = 0; e < 4; ++e) y[e] = __builtin_bit_cast(uint16_t, (__bf16)sum[e]);
+        if (whole) *reinterpret_cast<u16x4_any*>(a.Y + at) = y;
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (!whole && n + e < a.N) a.Y[at + e] = y[e];
       }
     }
   }
