@@ -192,7 +192,9 @@ def test_product_model_sizes(M, K, N, act):
 # Shapes of the tiled form: ragged in every direction, K that ends inside a stage and inside four
 # stages, scale rows that need padding, K split over workgroups, one and several rounds.
 TILED = [(520, 2080, 1001), (700, 1568, 1003), (257, 4160, 1000), (40, 17408, 1500), (300, 17440, 255), (513, 2016, 2050),
-         (1030, 1024, 1026), (2049, 640, 1030), (130, 8192, 1001), (4100, 512, 513), (48, 5120, 5119), (2047, 2048, 3000)]
+         (1030, 1024, 1026), (2049, 640, 1030), (130, 8192, 1001), (4100, 512, 513), (48, 5120, 5119), (2047, 2048, 3000),
+         # a workgroup takes several tiles in turn: four stages and more, K's last stage whole and not
+         (2047, 512, 17401), (2047, 480, 17401), (2047, 2016, 17401), (2048, 2048, 17408)]
 
 
 def _gpu_reference(X, W):
@@ -230,7 +232,7 @@ def test_product_tiled(M, K, N, act):
 
 
 @pytest.mark.parametrize("act", [16, 4])
-@pytest.mark.parametrize("M,K,N", [(520, 2080, 1001), (257, 4160, 1000), (40, 17408, 1500), (2047, 2048, 3000)])
+@pytest.mark.parametrize("M,K,N", [(520, 2080, 1001), (257, 4160, 1000), (40, 17408, 1500), (2047, 2048, 3000), (2047, 2016, 17401)])
 def test_product_tiled_special_values(M, K, N, act):
     """NaN scale bytes and non-finite activations in the tiled form, in the first and the last block
     of K: one channel or one row each, and nothing else."""

@@ -159,6 +159,7 @@ struct MxStreamPlan {
 };
 struct MxTilePlan {
   int tile, splits, stages;                // tile shape, split of K, 128-channel stages of a split
+  bool chain;                              // workgroups take several tiles in turn
 };
 MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N);
 MxTilePlan plan_mx_tile(int act_bits, int M, int K, int N);

@@ -41,6 +41,7 @@ struct MxTileArgs {
   const uint8_t* ws;        // [N][ss]
   int ss;                   // bytes of a scale row: a multiple of 4, at least 16
   int M, K, N;
+  int tiles;                // tiles of the output
   int stages_per_split;     // stages of blockIdx.y: [y, y + 1) * stages_per_split, a multiple of 4
   uint16_t* Y;              // [M][N], or
   float* partial;           // [splits][M][N] when not NULL
@@ -107,10 +108,11 @@ __device__ __forceinline__ void mx_store_rows(const MxTileArgs& a, const f32x4 (
   }
 }
 
-template <int FM, int FN>
+// SPLIT: the launch may write partial outputs.
+template <int FM, int FN, bool SPLIT>
 __device__ __forceinline__ void mx_store_tile(const MxTileArgs& a, const f32x4 (&acc)[FM][FN], int m1, int n1,
                                               unsigned char* stage) {
-  if (!a.partial) {
+  if (!SPLIT || !a.partial) {
     if ((a.N & 7) == 0) mx_store_rows<FM, FN, true>(a, acc, m1, n1, stage);
     else mx_store_rows<FM, FN, false>(a, acc, m1, n1, stage);
     return;
@@ -132,7 +134,11 @@ __device__ __forceinline__ void mx_store_tile(const MxTileArgs& a, const f32x4 (
 }
 
 // MXFP4 activations.  Four waves (2 x 2), one per SIMD, BM / 2 rows x BN / 2 channels each.
-template <int BM, int BN>
+// CHAIN: a workgroup takes the tiles blockIdx.x + i gridDim.x in turn, and the copies run on from one tile
+// to the next, so that a tile's outputs are stored while the next one's first stages arrive
+// (needs stages in fours, and M >= BM and N >= BN).  M = 2048, K = 2048, N = 17408: 47.3 us against 50.4;
+// K = 5120: 105.5 against 107.5, which is the power limit (88 on zeros); K = 1536, N = 17401: 40.9 against 47.8.
+template <int BM, int BN, bool CHAIN>
 __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   constexpr int W = 4;                          // waves
   static_assert(BM % 64 == 0 && BN % 64 == 0, "copies and scale copies cover 64 rows");
@@ -141,47 +147,65 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   constexpr int kSlot = kRows * 128, kScales = 2 * kSlot;
   constexpr int C = kRows / 8 / W;              // 1 KB copies (8 rows) per wave and pair of stages
   constexpr int CS = kRows / 16 / W;            // 1 KB copies (16 rows) per wave and 16 stages of scales
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * kSlot + kRows * 64];
+  // with CHAIN the outputs have LDS of their own: the slots belong to the next tile by then
+  constexpr int kOut = CHAIN ? kScales + kRows * 64 : 0;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[kScales + kRows * 64 + (CHAIN ? W * kMxStage<FN> : 0)];
   constexpr int kEvery = T / C;                 // matrix instructions per copy
   static_assert(kEvery >= 1 && C * kEvery < 2 * T, "a pair's copies fit two steps");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
   const int r = lane & 15, q = lane >> 4;
-  int tm, tn;
-  tile_coords(blockIdx.x, (a.M + BM - 1) / BM, (a.N + BN - 1) / BN, tm, tn);
-  const int m0 = tm * BM, n0 = tn * BN;
+  const int MT = (a.M + BM - 1) / BM, NT = (a.N + BN - 1) / BN;
   const int KB = a.K / kMxBlock, KT = (KB + 3) / 4;
   const int kt0 = blockIdx.y * a.stages_per_split, kt1 = min(KT, kt0 + a.stages_per_split);
   const int n_stages = kt1 - kt0;
   const int rem = KB & 3;                       // blocks of the last stage, 0: all four
   const uint32_t smem_base = (uint32_t)(uintptr_t)smem;
   const uint32_t rowb = (uint32_t)a.K / 2u;
-  const unsigned char* xb = static_cast<const unsigned char*>(a.X) + (size_t)m0 * rowb;
-  const unsigned char* wb = reinterpret_cast<const unsigned char*>(a.qweight) + (size_t)n0 * rowb;
-  const unsigned char* xsb = a.xs + (size_t)m0 * a.ss;
-  const unsigned char* wsb = a.ws + (size_t)n0 * a.ss;
-  const int mlast = a.M - 1 - m0, nlast = a.N - 1 - n0;
 
   // Stages travel in pairs, so that a row's piece is a whole 128-byte line (64-byte pieces
   // cost the L1 as much: 505 against 254 ns per 32 KB and CU).  Copy u of this wave is
   // unit wave + 4 u: rows 8 (wave + 4 u) + lane / 8, position lane % 8 holding chunk
   // (lane % 8) ^ ((row >> 1) & 7), the same for every u.
-  uint32_t off[C], soff[CS];
+  // With CHAIN a tile at the edge moves back inside, so that one lane offset serves every copy (it
+  // computes outputs that its neighbour has too, the same bits); otherwise rows past the
+  // edge re-read the last one.
+  constexpr int kOff = CHAIN ? 1 : C, kSoff = CHAIN ? 1 : CS;
+  uint32_t off[kOff], soff[kSoff];
+  const unsigned char *xb, *wb, *xsb, *wsb;
+  int m0, n0;                                   // the tile that copies are made of
   auto is_x = [](int u) { return u < BM / 8 / W; };            // compile-time: activations first
+  auto set_tile = [&](int tile) {
+    int tm, tn;
+    tile_coords(tile, MT, NT, tm, tn);
+    m0 = CHAIN ? min(tm * BM, a.M - BM) : tm * BM;
+    n0 = CHAIN ? min(tn * BN, a.N - BN) : tn * BN;
+    xb = static_cast<const unsigned char*>(a.X) + (size_t)m0 * rowb;
+    wb = reinterpret_cast<const unsigned char*>(a.qweight) + (size_t)n0 * rowb;
+    xsb = a.xs + (size_t)m0 * a.ss;
+    wsb = a.ws + (size_t)n0 * a.ss;
+  };
+  set_tile(blockIdx.x);
+  if constexpr (CHAIN) {
+    off[0] = (uint32_t)(wave * 8 + (lane >> 3)) * rowb;
+    soff[0] = (uint32_t)(wave * 16 + (lane >> 2)) * (uint32_t)a.ss;
+  } else {
+    const int mlast = a.M - 1 - m0, nlast = a.N - 1 - n0;
 #pragma unroll
-  for (int u = 0; u < C; ++u) {
-    const int row = (wave + W * u) * 8 + (lane >> 3) - (is_x(u) ? 0 : BM);
-    off[u] = (uint32_t)min(row, is_x(u) ? mlast : nlast) * rowb;
-  }
+    for (int u = 0; u < C; ++u) {
+      const int row = (wave + W * u) * 8 + (lane >> 3) - (is_x(u) ? 0 : BM);
+      off[u % kOff] = (uint32_t)min(row, is_x(u) ? mlast : nlast) * rowb;
+    }
 #pragma unroll
-  for (int u = 0; u < CS; ++u) {
-    const int row = (wave + W * u) * 16 + (lane >> 2) - (u < BM / 16 / W ? 0 : BM);
-    soff[u] = (uint32_t)min(row, u < BM / 16 / W ? mlast : nlast) * (uint32_t)a.ss;
+    for (int u = 0; u < CS; ++u) {
+      const int row = (wave + W * u) * 16 + (lane >> 2) - (u < BM / 16 / W ? 0 : BM);
+      soff[u % kSoff] = (uint32_t)min(row, u < BM / 16 / W ? mlast : nlast) * (uint32_t)a.ss;
+    }
   }
   const int chunk = (lane & 7) ^ (((wave * 8 + (lane >> 3)) >> 1) & 7);
-  // Copies of pair p of stages counted from kt0, into slot p % 2; past the end the last
-  // pair is copied again, into a slot that nothing reads any more.
+  // Copies of pair p of stages counted from kt0, into slot p % 2; past the end of the last tile
+  // its last pair is copied again, into a slot that nothing reads any more.
   struct Src {
     const unsigned char *x, *w;
     uint32_t c;
@@ -191,7 +215,9 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
     return Src{xb + (size_t)kt * 64, wb + (size_t)kt * 64, 16u * (uint32_t)min(chunk, min(8, KB - 4 * kt) - 1)};
   };
   auto copy = [&](const Src& s, int slot, int u) {
-    lds_copy16(off[u] + s.c, is_x(u) ? s.x : s.w, smem_base + (uint32_t)(slot * kSlot + (wave + W * u) * 1024));
+    const uint32_t rows = CHAIN ? W * 8 * (is_x(u) ? u : u - BM / 8 / W) : 0;
+    lds_copy16(off[u % kOff] + rows * rowb + s.c, is_x(u) ? s.x : s.w, 
+               smem_base + (uint32_t)(slot * kSlot + (wave + W * u) * 1024));
   };
   // A group's (four stages') first stage, moved back where the row ends before the group does.
   auto group_start = [&](int group) { return max(0, min(kt0 + 4 * group, KT - 4)); };
@@ -201,15 +227,21 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   auto copy_scales = [&](int b) {
     const uint32_t c = 4u * (uint32_t)group_start(4 * b + ((lane & 3) ^ ((lane >> 4) & 3)));
 #pragma unroll
-    for (int u = 0; u < CS; ++u)
-      lds_copy16(soff[u] + c, u < BM / 16 / W ? xsb : wsb, smem_base + (uint32_t)(kScales + (wave + W * u) * 1024));
+    for (int u = 0; u < CS; ++u) {
+      const bool x = u < BM / 16 / W;
+      const uint32_t rows = CHAIN ? W * 16 * (x ? u : u - BM / 16 / W) : 0;
+      lds_copy16(soff[u % kSoff] + rows * (uint32_t)a.ss + c, x ? xsb : wsb,
+                 smem_base + (uint32_t)(kScales + (wave + W * u) * 1024));
+    }
   };
 
   f32x4 acc[FM][FN];
+  auto clear = [&] {
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
   // fragment e: channels for e < FN, activation rows after; row 16 e' + r of this wave's
   // part ((row >> 1) & 7 does not depend on e'), chunk 4 h + q of the pair's stage h
   const uint32_t swz = (uint32_t)((q ^ ((r >> 1) & 7)) * 16);
@@ -237,7 +269,9 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   // stage's (scales: the next four stages').  So a pair's slot is free when its second stage
   // starts: that step waits for the next pair, meets the other waves and refills the
   // slot, copies first, two stages before they are needed.
-  auto step = [&](auto jc, int s) {
+  // `ahead`: what is copied and read from here on belongs to the next tile (the last three of a
+  // tile's stages).
+  auto step = [&](auto jc, int s, bool ahead) {
     constexpr int J = decltype(jc)::value;
     constexpr int cur = J & 1, nxt = cur ^ 1;
     const int stage = s + J;
@@ -245,7 +279,8 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
       wait_vmcnt<0>();
       mx_barrier();
     }
-    const Src src = source((stage >> 1) + (cur == 1 ? 2 : 1));
+    const int pair = (stage >> 1) + (cur == 1 ? 2 : 1);
+    const Src src = source(ahead ? pair - (n_stages >> 1) : pair);
     if (rem != 0 && kt0 + stage == KT - 1 && q >= rem) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) f[cur][j] = u32x4{0, 0, 0, 0};
@@ -258,7 +293,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
     constexpr int kReads = F + (J == 3 ? F + kLag : 0);
     constexpr int kPer = (kReads + T - 1) / T;  // more than one where the tile is small
     u32x4 raw[F];
-    const int group = (stage + 1) >> 2, shift = J == 3 ? shift_of(group) : 0;
+    const int group = ahead ? 0 : (stage + 1) >> 2, shift = J == 3 ? shift_of(group) : 0;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const int tc = cur == 1 ? t : T + t;      // matrix instructions since the pair's slot was free
@@ -266,7 +301,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
         const int u = tc / kEvery;
         constexpr int slot = cur == 1 ? J >> 1 : (J >> 1) ^ 1;
         // the last group of the scales in LDS is in registers by now
-        if (u == 0) { if (J == 1 && ((stage + 3) & 15) == 0) copy_scales((stage + 3) >> 4); }
+        if (u == 0) { if (J == 1 && (ahead || ((stage + 3) & 15) == 0)) copy_scales(ahead ? 0 : (stage + 3) >> 4); }
         else copy(src, slot, u - 1);
       }
 #pragma unroll
@@ -291,6 +326,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   };
 
   constexpr int kEarly = (T - 1) / kEvery < C ? (T - 1) / kEvery : C;
+  int tile = blockIdx.x;
   copy_scales(0);
   {
     const Src p0 = source(0), p1 = source(1);
@@ -307,15 +343,29 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
     read(0, 0, e);
     sc[e] = pack_bytes(read_scales(0, e), sel) >> shift_of(0);
   }
-  for (int s = 0; s < n_stages; s += 4) {
-    step(std::integral_constant<int, 0>{}, s);
-    if (s + 1 < n_stages) step(std::integral_constant<int, 1>{}, s);
-    if (s + 2 < n_stages) step(std::integral_constant<int, 2>{}, s);
-    if (s + 3 < n_stages) step(std::integral_constant<int, 3>{}, s);
+  for (;;) {
+    const int next = tile + (int)gridDim.x;
+    const bool more = CHAIN && next < a.tiles;
+    const int m = m0 + wm * FM * 16, n = n0 + wn * FN * 16;
+    clear();
+    for (int s = 0; s < n_stages; s += 4) {
+      const bool ahead = more && s + 4 >= n_stages;
+      // the conditions also keep the compiler from moving a step's products into a later one
+      step(std::integral_constant<int, 0>{}, s, false);
+      if (ahead) set_tile(next);
+      if (s + 1 < n_stages) step(std::integral_constant<int, 1>{}, s, ahead);
+      if (s + 2 < n_stages) step(std::integral_constant<int, 2>{}, s, ahead);
+      if (s + 3 < n_stages) step(std::integral_constant<int, 3>{}, s, ahead);
+    }
+    if constexpr (!CHAIN) {
+      wait_vmcnt<0>();
+      lds_barrier();                            // no copy and no read of the slots is left
+    }
+    mx_store_tile<FM, FN, !CHAIN>(a, acc, m, n, smem + kOut + wave * kMxStage<FN>);
+    if (!more) break;
+    tile = next;
   }
-  wait_vmcnt<0>();
-  lds_barrier();                                // no copy and no read of the slots is left
-  mx_store_tile<FM, FN>(a, acc, m0 + wm * FM * 16, n0 + wn * FN * 16, smem + wave * kMxStage<FN>);
+  wait_vmcnt<0>();                              // copies past the end
 }
 
 // bf16 activations.  Four waves (2 x 2), one per SIMD, BM / 2 rows x BN / 2 channels each.
@@ -512,7 +562,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a16_kernel(MxTileArgs a) {
   }
   wait_vmcnt<0>();
   lds_barrier();                                // no copy and no read of the slots is left
-  mx_store_tile<FM, FN>(a, acc, m0 + wm * FM * 16, n0 + wn * FN * 16, smem + wave * kMxStage<FN>);
+  mx_store_tile<FM, FN, true>(a, acc, m0 + wm * FM * 16, n0 + wn * FN * 16, smem + wave * kMxStage<FN>);
 }
 
 }  // namespace w4
