@@ -26,8 +26,9 @@
 // 64 pieces of 16 bytes, four times the cache lines.  Chunk k of column c is at position k ^
 // mx_swizzle16(c), so that both sides are free of bank conflicts.
 // Loads are range-checked buffer loads: rows past M and N and blocks past K read
-// zeros and touch no memory.  The whole offset is in the checked lane offset: the scalar
-// one of these instructions is added after the check.
+// zeros and touch no memory.  A tile's first row is the scalar offset of the loads, which is not
+// relied on to be part of the check: a tile that would end past the last row moves back to
+// end there, and has some outputs (the same bits) in common with the tile before.
 #include <algorithm>
 
 #include "mxfp4.hpp"
@@ -84,7 +85,7 @@ __global__ __launch_bounds__(kMxStreamWaves * 64) void mx_stream_kernel(MxStream
 
   constexpr int XV = ACT == 16 ? 4 : 1;        // 16-byte loads of an activation tile per lane and step
   const uint32_t wo = (uint32_t)(r / SL) * (uint32_t)(a.K / 2), so = (uint32_t)(r / SL) * (uint32_t)KB;
-  const uint32_t wstep = (uint32_t)kCh * (uint32_t)(a.K / 2), sstep = (uint32_t)kCh * (uint32_t)KB;
+  auto tile_row = [](int tile, int rows) { return max(0, min(tile * kCh, rows - kCh)); };   // of `rows` in all
   const int kq = 4 * (r % SL) + q;             // block of this lane's weights within a step
   // ACT = 16: load v of a tile covers columns 4 v + q, lane r its chunk r (8 channels);
   // ACT = 4: the lane's own column r and block q.
@@ -97,7 +98,12 @@ __global__ __launch_bounds__(kMxStreamWaves * 64) void mx_stream_kernel(MxStream
     xo[v] = (uint32_t)(c / SL) * xbytes + (ACT == 16 ? (uint32_t)(c % SL) * 256u + 16u * r : 16u * kq);
     xk[v] = ACT == 16 ? 4 * (c % SL) + r / 4 : kq;
   }
-  const uint32_t xtile = (uint32_t)kCh * xbytes;
+
+  int wrow[CB], xrow[RB];
+#pragma unroll
+  for (int j = 0; j < CB; ++j) wrow[j] = tile_row(j, nrows);
+#pragma unroll
+  for (int i = 0; i < RB; ++i) xrow[i] = tile_row(i, mrows);
 
   struct Step {
     u32x4 w[CB], x[RB][XV];
@@ -109,20 +115,20 @@ __global__ __launch_bounds__(kMxStreamWaves * 64) void mx_stream_kernel(MxStream
     const uint32_t wk = kq < left ? wo + 16u * (kb + kq) : kOob, sk = kq < left ? so + kb + kq : kOob;
 #pragma unroll
     for (int j = 0; j < CB; ++j) {
-      s.w[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wk + j * wstep, 0, 0));
-      s.ws[j] = __builtin_amdgcn_raw_buffer_load_b8(rs, sk + j * sstep, 0, 0);
+      s.w[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wk, wrow[j] * (a.K / 2), 0));
+      s.ws[j] = __builtin_amdgcn_raw_buffer_load_b8(rs, sk, wrow[j] * KB, 0);
     }
 #pragma unroll
     for (int v = 0; v < XV; ++v) {
       const uint32_t o = xk[v] < left ? xo[v] + (ACT == 16 ? 64u : 16u) * kb : kOob;
 #pragma unroll
       for (int i = 0; i < RB; ++i)
-        s.x[i][v] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, o + i * xtile, 0, 0));
+        s.x[i][v] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, o, xrow[i] * (int)xbytes, 0));
     }
     if constexpr (ACT == 4) {
 #pragma unroll
       for (int i = 0; i < RB; ++i)
-        s.xs[i] = __builtin_amdgcn_raw_buffer_load_b8(rxs, sk + i * sstep, 0, 0);
+        s.xs[i] = __builtin_amdgcn_raw_buffer_load_b8(rxs, sk, xrow[i] * KB, 0);
     }
   };
 
@@ -211,7 +217,7 @@ __global__ __launch_bounds__(kMxStreamWaves * 64) void mx_stream_kernel(MxStream
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] += p[e];
       }
-      const int m = m0 + kCh * i + row, n = n0 + c;
+      const int m = m0 + xrow[i] + row, n = n0 + tile_row(c / kCh, nrows) + c % kCh;
       if (m >= a.M) continue;
       const size_t at = (size_t)m * a.N + n;
       const bool whole = n + 4 <= a.N;           // four outputs at once, aligned to one
@@ -333,7 +339,8 @@ int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t str
 }
 
 // The tiled form with 4-bit activations from 17 rows on (K = 2048, N = 6144: M = 20 5.4 against 5.8,
-// M = 64 5.6 against 9.0), 33 on small weights (K = N = 2048, M = 20: 5.3 against 4.8); with bf16
+// M = 64 5.6 against 9.0), 33 on small weights (K = N = 2048, M = 20: 5.3 against 4.8), 9 on large
+// ones (K = 5120, N = 17408, M = 9 13.2 against 16.9, M = 16 14.3 against 17.0); with bf16
 // ones where more than 32 rows and 10^9 products meet (K = 2048, N = 6144: M = 64 11.1 against
 // 9.0, M = 128 12.3 against 15.9; K = 5120, N = 17408: M = 32 29 against 24, M = 64 33 against 35).
 // Where scale rows have to be padded first, by another launch, it has to be worth that
@@ -343,7 +350,7 @@ bool mxfp4_use_tile(int act_bits, int M, int K, int N) {
   if (act_bits == 16) return M > 32 && MNK >= 1e9;
   const int KB = K / kMxBlock;
   if (KB % 4 != 0 || KB < 16) return MNK >= 2e9;
-  return M > (NK >= 8e6 ? 16 : 32);
+  return M > (NK >= 6e7 ? 8 : NK >= 8e6 ? 16 : 32);
 }
 
 MxPlan plan_mxfp4_gemm(int act_bits, int M, int K, int N) {
