@@ -194,7 +194,9 @@ def test_product_model_sizes(M, K, N, act):
 TILED = [(520, 2080, 1001), (700, 1568, 1003), (257, 4160, 1000), (40, 17408, 1500), (300, 17440, 255), (513, 2016, 2050),
          (1030, 1024, 1026), (2049, 640, 1030), (130, 8192, 1001), (4100, 512, 513), (48, 5120, 5119), (2047, 2048, 3000),
          # a workgroup takes several tiles in turn: four stages and more, K's last stage whole and not
-         (2047, 512, 17401), (2047, 480, 17401), (2047, 2016, 17401), (2048, 2048, 17408)]
+         (2047, 512, 17401), (2047, 480, 17401), (2047, 2016, 17401), (2048, 2048, 17408),
+         # the large tiles with one tile per workgroup, K split and not
+         (1564, 17344, 2577), (940, 6784, 13941), (8691, 1920, 2764), (668, 9792, 6229)]
 
 
 def _gpu_reference(X, W):
@@ -232,7 +234,7 @@ def test_product_tiled(M, K, N, act):
 
 
 @pytest.mark.parametrize("act", [16, 4])
-@pytest.mark.parametrize("M,K,N", [(520, 2080, 1001), (257, 4160, 1000), (40, 17408, 1500), (2047, 2048, 3000), (2047, 2016, 17401)])
+@pytest.mark.parametrize("M,K,N", [(520, 2080, 1001), (257, 4160, 1000), (40, 17408, 1500), (2047, 2048, 3000), (2047, 2016, 17401), (940, 6752, 13941)])
 def test_product_tiled_special_values(M, K, N, act):
     """NaN scale bytes and non-finite activations in the tiled form, in the first and the last block
     of K: one channel or one row each, and nothing else."""
