@@ -29,19 +29,16 @@ struct MxTile {
   int bm, bn, occ;
   float start, alone, full;
 };
-constexpr MxTile kTiles4[] = {{256, 256, 1, 8.0f, 0.80f, 0.80f}, {256, 192, 1, 6.0f, 0.64f, 0.64f},
-                              {128, 128, 2, 3.0f, 0.33f, 0.54f}, {128, 64, 2, 2.0f, 0.27f, 0.37f},
+constexpr MxTile kTiles4[] = {{256, 256, 1, 7.0f, 0.87f, 0.87f}, {256, 192, 1, 5.5f, 0.67f, 0.67f},
+                              {128, 128, 2, 3.0f, 0.36f, 0.54f}, {128, 64, 2, 2.0f, 0.27f, 0.37f},
                               {64, 64, 4, 1.5f, 0.25f, 0.45f}};
 constexpr MxTile kTiles16[] = {{256, 192, 1, 6.0f, 2.48f, 2.48f}, {128, 128, 1, 3.2f, 0.88f, 0.97f},
                                {128, 64, 2, 2.4f, 0.62f, 1.03f}, {64, 64, 3, 1.7f, 0.50f, 1.16f}};
 constexpr int kCus = 256;
-// More than one round of the 256 x 192 tile may be chained.  What that gains, in microseconds per further
-// round: a tile's outputs (more where they are not aligned) leave under the next one's first stages, but
-// the chained form is 16 x 16 (32 x 32 with it lacks registers) and a little slower per stage.  M = 2048,
-// N = 17408: K = 2048 46.8 chained against 49.2, 3584 72.1 against 74.8, 4096 78.8 against 77.1, 5120 106 against 102;
-// N = 17401: K = 2048 46.8 against 53.9, 5120 101 against 109.
+// More than one round of the 256 x 192 tile is chained where K allows it: a further tile starts so much sooner.
+// (A single round keeps the other form, 41.3 against 42.3 us at K = 6144.)
 constexpr int kChained = 1;
-double chain_gain(int KT, int N) { return (N % 8 ? 3.5 : 1.3) - 0.04 * KT; }
+constexpr double kChainGain = 1.5;
 
 double tile_cost(const MxTile& t, long long wgs, int stages) {
   const long long round = (long long)t.occ * kCus;
@@ -75,8 +72,8 @@ MxTilePlan plan_mx_tile(int act_bits, int M, int K, int N) {
       if (splits > 1 && actual < splits) break;
       double us = tile_cost(tiles[i], n * actual, stages);
       const bool chain = act_bits == 4 && i == kChained && splits == 1 && n > kCus && KT % 4 == 0 &&
-                         M >= tiles[i].bm && N >= tiles[i].bn && chain_gain(KT, N) > 0;
-      if (chain) us -= chain_gain(KT, N) * (double)((n - 1) / kCus);
+                         M >= tiles[i].bm && N >= tiles[i].bn;
+      if (chain) us -= kChainGain * (double)((n - 1) / kCus);
       // a split's partial outputs are written and read once, by another launch
       if (actual > 1) us += 3.0 + 8.0 * actual * M * N / 3.0e6;
       if (us < best_us) {
@@ -142,14 +139,14 @@ int launch_mx_tile(const MxTilePlan& p, const MxGemmArgs& g, hipStream_t stream)
   const dim3 grid((unsigned)a.tiles, (unsigned)p.splits), block(256);
   if (g.act_bits == 4) {
     switch (p.tile) {
-      case 0: hipLaunchKernelGGL((mx_tile_a4_kernel<256, 256, 32, false>), grid, block, 0, stream, a); break;
+      case 0: hipLaunchKernelGGL((mx_tile_a4_kernel<256, 256, false>), grid, block, 0, stream, a); break;
       case 1:
-        if (p.chain) hipLaunchKernelGGL((mx_tile_a4_kernel<256, 192, 16, true>), dim3(kCus), block, 0, stream, a);
-        else hipLaunchKernelGGL((mx_tile_a4_kernel<256, 192, 32, false>), grid, block, 0, stream, a);
+        if (p.chain) hipLaunchKernelGGL((mx_tile_a4_kernel<256, 192, true>), dim3(kCus), block, 0, stream, a);
+        else hipLaunchKernelGGL((mx_tile_a4_kernel<256, 192, false>), grid, block, 0, stream, a);
         break;
-      case 2: hipLaunchKernelGGL((mx_tile_a4_kernel<128, 128, 16, false>), grid, block, 0, stream, a); break;
-      case 3: hipLaunchKernelGGL((mx_tile_a4_kernel<128, 64, 16, false>), grid, block, 0, stream, a); break;
-      default: hipLaunchKernelGGL((mx_tile_a4_kernel<64, 64, 16, false>), grid, block, 0, stream, a); break;
+      case 2: hipLaunchKernelGGL((mx_tile_a4_kernel<128, 128, false>), grid, block, 0, stream, a); break;
+      case 3: hipLaunchKernelGGL((mx_tile_a4_kernel<128, 64, false>), grid, block, 0, stream, a); break;
+      default: hipLaunchKernelGGL((mx_tile_a4_kernel<64, 64, false>), grid, block, 0, stream, a); break;
     }
   } else {
     switch (p.tile) {

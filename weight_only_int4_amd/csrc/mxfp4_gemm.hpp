@@ -13,8 +13,7 @@
 // tile's side.  What two waves would overlap, the single one overlaps itself: between its
 // matrix instructions it reads the next stage's fragments and issues copies.  Measured at
 // M = 2048, K = 5120, N = 17408, 4-bit: eight waves in one phase 179 us, two waves per SIMD in
-// opposite phases 152, this 102 (3.6 PFLOP/s; on zeros 85, the rest is power; the matrix
-// instructions alone, on random data, 56).
+// opposite phases 152, this 106 (3.4 PFLOP/s; the matrix instructions alone, on random data, 56).
 //
 // LDS layout: position p of a row holds its 16-byte chunk p ^ f(row), with f chosen for each
 // row length so that every pass of a fragment read covers all 64 banks once (measured with
@@ -62,141 +61,106 @@ __device__ __forceinline__ uint32_t pack_bytes(u32x4 d, uint32_t sel) {
   return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
 }
 
-// Accumulators of one matrix instruction, R x R outputs.  The lane's activation row is lane % R, and
-// its channels come in quads: quad g at channel mx_quad<R>(g, lane / R).
-template <int R>
-struct MxAcc;
-template <>
-struct MxAcc<16> {
-  typedef f32x4 type;
-};
-template <>
-struct MxAcc<32> {
-  typedef float type __attribute__((ext_vector_type(16)));
-};
-template <int R>
-__device__ __forceinline__ int mx_quad(int g, int q) {
-  return R == 16 ? 4 * q : 8 * g + 4 * q;
-}
-
-// The tile's outputs.  A store straight from the lanes' quads would write 8-byte pieces, so bf16 rows go
-// through `stage`, this wave's own kMxStage<N> bytes of LDS (16 rows of N channels, padded by 16
-// bytes against bank conflicts), and leave in 16-byte pieces of whole rows.
-template <int N>
-constexpr int kMxStage = 16 * (N * 2 + 16);
+// The tile's outputs: lane (c, q) of tile (i, j) holds row c, channels 4 q .. 4 q + 3, so
+// a store straight from there writes 32-byte pieces.  bf16 rows go through `stage`, this
+// wave's own kMxStage<FN> bytes of LDS (16 rows, padded by 16 bytes against bank
+// conflicts), and leave in 16-byte pieces of whole rows.
+template <int FN>
+constexpr int kMxStage = 16 * (FN * 32 + 16);
 
 // Where N is not a multiple of eight (WHOLE false) the pieces are not aligned, and the last one
 // of a row goes element by element.  (Aligned pieces of one element instead: M = 2047, K = 1536, N = 17401 took
 // 83 us against 48.)
-template <int R, int FM, int FN, bool WHOLE, bool TIGHT>
-__device__ __forceinline__ void mx_store_rows(const MxTileArgs& a, const typename MxAcc<R>::type (&acc)[FM][FN], int m1,
-                                              int n1, unsigned char* stage) {
+template <int FM, int FN, bool WHOLE>
+__device__ __forceinline__ void mx_store_rows(const MxTileArgs& a, const f32x4 (&acc)[FM][FN], int m1, int n1,
+                                              unsigned char* stage) {
   typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
   typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
   typedef u16x8 u16x8_unaligned __attribute__((aligned(2)));
-  constexpr int kRow = FN * R * 2 + 16, kPieces = FN * R / 8;
-  int lane = threadIdx.x & 63;
-  if constexpr (TIGHT) {                        // keeps the addresses below from living through the main loop
-    asm volatile("" : "+v"(lane));
-    lane &= 63;
-  }
-  const int r = lane % R, q = lane / R, N = a.N;
+  constexpr int kRow = FN * 32 + 16, kPieces = FN * 2;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
 #pragma unroll
-  for (int i = 0; i < FM * R / 16; ++i) {       // 16 rows at a time
-    if (R == 16 || (r >> 4) == (i & 1)) {
+  for (int i = 0; i < FM; ++i) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int g = 0; g < R * R / 256; ++g) {
-          const auto& v = acc[i * 16 / R][j];
-          const bf16x4 b = {(__bf16)v[4 * g], (__bf16)v[4 * g + 1], (__bf16)v[4 * g + 2], (__bf16)v[4 * g + 3]};
-          *reinterpret_cast<bf16x4*>(stage + (r & 15) * kRow + (j * R + mx_quad<R>(g, q)) * 2) = b;
-        }
+    for (int j = 0; j < FN; ++j) {
+      const bf16x4 b = {(__bf16)acc[i][j][0], (__bf16)acc[i][j][1], (__bf16)acc[i][j][2], (__bf16)acc[i][j][3]};
+      *reinterpret_cast<bf16x4*>(stage + r * kRow + j * 32 + q * 8) = b;
     }
     __builtin_amdgcn_wave_barrier();            // LDS operations of one wave complete in order
 #pragma unroll
     for (int p = lane; p < 16 * kPieces; p += 64) {
       const int row = p / kPieces, c = p % kPieces;
       const int m = m1 + 16 * i + row, n = n1 + 8 * c;
-      if (m >= a.M || n >= N) continue;
-      uint16_t* y = a.Y + (size_t)m * N + n;
+      if (m >= a.M || n >= a.N) continue;
+      uint16_t* y = a.Y + (size_t)m * a.N + n;
       const u16x8 v = *reinterpret_cast<const u16x8*>(stage + row * kRow + c * 16);
       if (WHOLE) {
         *reinterpret_cast<u16x8*>(y) = v;
-      } else if (n + 8 <= N) {
+      } else if (n + 8 <= a.N) {
         *reinterpret_cast<u16x8_unaligned*>(y) = v;
       } else {
 #pragma unroll
         for (int e = 0; e < 7; ++e)
-          if (n + e < N) y[e] = v[e];
+          if (n + e < a.N) y[e] = v[e];
       }
     }
     __builtin_amdgcn_wave_barrier();
-    if (TIGHT) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
 // SPLIT: the launch may write partial outputs.
-template <int R, bool SPLIT, int FM, int FN>
-__device__ __forceinline__ void mx_store_tile(const MxTileArgs& a, const typename MxAcc<R>::type (&acc)[FM][FN], int m1,
-                                              int n1, unsigned char* stage) {
+template <int FM, int FN, bool SPLIT>
+__device__ __forceinline__ void mx_store_tile(const MxTileArgs& a, const f32x4 (&acc)[FM][FN], int m1, int n1,
+                                              unsigned char* stage) {
   if (!SPLIT || !a.partial) {
-    if ((a.N & 7) == 0) mx_store_rows<R, FM, FN, true, !SPLIT>(a, acc, m1, n1, stage);
-    else mx_store_rows<R, FM, FN, false, !SPLIT>(a, acc, m1, n1, stage);
+    if ((a.N & 7) == 0) mx_store_rows<FM, FN, true>(a, acc, m1, n1, stage);
+    else mx_store_rows<FM, FN, false>(a, acc, m1, n1, stage);
     return;
   }
-  const int lane = threadIdx.x & 63, r = lane % R, q = lane / R;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   float* part = a.partial + (size_t)blockIdx.y * a.M * a.N;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int m = m1 + R * i + r;
+    const int m = m1 + 16 * i + r;
     if (m >= a.M) continue;
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+    for (int j = 0; j < FN; ++j) {
+      const int n = n1 + 16 * j + 4 * q;
 #pragma unroll
-      for (int g = 0; g < R * R / 256; ++g) {
-        const int n = n1 + R * j + mx_quad<R>(g, q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < a.N) part[(size_t)m * a.N + n + e] = acc[i][j][4 * g + e];
-      }
+      for (int e = 0; e < 4; ++e)
+        if (n + e < a.N) part[(size_t)m * a.N + n + e] = acc[i][j][e];
+    }
   }
 }
 
-// MXFP4 activations.  Four waves (2 x 2), one per SIMD, BM / 2 rows x BN / 2 channels each, in matrix
-// instructions of R x R outputs: 32 x 32 x 64 for the large tiles (half as many to issue, so that the
-// reads, copies and scalar work between them find room: 256 x 192 at M = 2048, K = 6144, N = 6144 39.3 us against
-// 40.8, 256 x 256 at N = 8192 49.8 against 52.7, 4.1 PFLOP/s), 16 x 16 x 128 for the small ones.
+// MXFP4 activations.  Four waves (2 x 2), one per SIMD, BM / 2 rows x BN / 2 channels each.
 // CHAIN: a workgroup takes the tiles blockIdx.x + i gridDim.x in turn, and the copies run on from one tile
 // to the next, so that a tile's outputs are stored while the next one's first stages arrive
-// (needs stages in fours, and M >= BM and N >= BN).
-template <int BM, int BN, int R, bool CHAIN>
+// (needs stages in fours, and M >= BM and N >= BN).  M = 2048, K = 2048, N = 17408: 47.3 us against 50.4;
+// K = 5120: 105.5 against 107.5, which is the power limit (88 on zeros); K = 1536, N = 17401: 40.9 against 47.8.
+template <int BM, int BN, bool CHAIN>
 __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   constexpr int W = 4;                          // waves
   static_assert(BM % 64 == 0 && BN % 64 == 0, "copies and scale copies cover 64 rows");
-  constexpr int FM = BM / 2 / R, FN = BN / 2 / R, F = FM + FN;
-  constexpr int H = R / 16;                     // matrix instructions along a stage's four blocks
-  constexpr int T = FM * FN * H;
+  constexpr int FM = BM / 32, FN = BN / 32, F = FM + FN, T = FM * FN;
   constexpr int kRows = BM + BN;                // activation rows, then channels
   constexpr int kSlot = kRows * 128, kScales = 2 * kSlot;
   constexpr int C = kRows / 8 / W;              // 1 KB copies (8 rows) per wave and pair of stages
   constexpr int CS = kRows / 16 / W;            // 1 KB copies (16 rows) per wave and 16 stages of scales
   // with CHAIN the outputs have LDS of their own: the slots belong to the next tile by then
   constexpr int kOut = CHAIN ? kScales + kRows * 64 : 0;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[kScales + kRows * 64 + (CHAIN ? W * kMxStage<BN / 2> : 0)];
-  constexpr int kEvery = (2 * T + C) / (2 * C); // matrix instructions per copy: about a step for a pair's
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[kScales + kRows * 64 + (CHAIN ? W * kMxStage<FN> : 0)];
+  constexpr int kEvery = T / C;                 // matrix instructions per copy
   static_assert(kEvery >= 1 && C * kEvery < 2 * T, "a pair's copies fit two steps");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
-  const int r = lane % R, q = lane / R;
+  const int r = lane & 15, q = lane >> 4;
   const int MT = (a.M + BM - 1) / BM, NT = (a.N + BN - 1) / BN;
   const int KB = a.K / kMxBlock, KT = (KB + 3) / 4;
   const int kt0 = blockIdx.y * a.stages_per_split, kt1 = min(KT, kt0 + a.stages_per_split);
   const int n_stages = kt1 - kt0;
-  const int rem = KB & 3;                       // blocks of K's last stage, 0: all four
-  const int ragged = rem != 0 ? KT - 1 - kt0 : -1;             // that stage, where it is not whole
-  const int pairs = (n_stages + 1) >> 1;
+  const int rem = KB & 3;                       // blocks of the last stage, 0: all four
   const uint32_t smem_base = (uint32_t)(uintptr_t)smem;
   const uint32_t rowb = (uint32_t)a.K / 2u;
 
@@ -211,16 +175,14 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   uint32_t off[kOff], soff[kSoff];
   const unsigned char *xb, *wb, *xsb, *wsb;
   int m0, n0;                                   // the tile that copies are made of
-  int pair;                                     // the pair that copies are made of; xb and wb point to it
   auto is_x = [](int u) { return u < BM / 8 / W; };            // compile-time: activations first
   auto set_tile = [&](int tile) {
     int tm, tn;
     tile_coords(tile, MT, NT, tm, tn);
     m0 = CHAIN ? min(tm * BM, a.M - BM) : tm * BM;
     n0 = CHAIN ? min(tn * BN, a.N - BN) : tn * BN;
-    pair = 0;
-    xb = static_cast<const unsigned char*>(a.X) + (size_t)m0 * rowb + (size_t)kt0 * 64;
-    wb = reinterpret_cast<const unsigned char*>(a.qweight) + (size_t)n0 * rowb + (size_t)kt0 * 64;
+    xb = static_cast<const unsigned char*>(a.X) + (size_t)m0 * rowb;
+    wb = reinterpret_cast<const unsigned char*>(a.qweight) + (size_t)n0 * rowb;
     xsb = a.xs + (size_t)m0 * a.ss;
     wsb = a.ws + (size_t)n0 * a.ss;
   };
@@ -242,19 +204,19 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
     }
   }
   const int chunk = (lane & 7) ^ (((wave * 8 + (lane >> 3)) >> 1) & 7);
-  // Lane offset of the chunk in a whole pair, and in the last one, where lanes past K copy its last block.
-  const uint32_t whole = 16u * (uint32_t)chunk;
-  const uint32_t last = 16u * (uint32_t)min(chunk, min(8, KB - 4 * (kt0 + ((n_stages - 1) & ~1))) - 1);
-  // Past the end of the last tile its last pair is copied again, into a slot that nothing reads any more.
-  auto next_pair = [&] {
-    const int step = pair + 1 < pairs ? 1 : 0;
-    pair += step;
-    xb += 128 * step;
-    wb += 128 * step;
+  // Copies of pair p of stages counted from kt0, into slot p % 2; past the end of the last tile
+  // its last pair is copied again, into a slot that nothing reads any more.
+  struct Src {
+    const unsigned char *x, *w;
+    uint32_t c;
   };
-  auto copy = [&](int slot, int u) {
+  auto source = [&](int pair) {
+    const int kt = kt0 + 2 * min(pair, (n_stages - 1) >> 1);
+    return Src{xb + (size_t)kt * 64, wb + (size_t)kt * 64, 16u * (uint32_t)min(chunk, min(8, KB - 4 * kt) - 1)};
+  };
+  auto copy = [&](const Src& s, int slot, int u) {
     const uint32_t rows = CHAIN ? W * 8 * (is_x(u) ? u : u - BM / 8 / W) : 0;
-    lds_copy16(off[u % kOff] + rows * rowb + (pair + 1 < pairs ? whole : last), is_x(u) ? xb : wb,
+    lds_copy16(off[u % kOff] + rows * rowb + s.c, is_x(u) ? s.x : s.w, 
                smem_base + (uint32_t)(slot * kSlot + (wave + W * u) * 1024));
   };
   // A group's (four stages') first stage, moved back where the row ends before the group does.
@@ -273,41 +235,32 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
     }
   };
 
-  typename MxAcc<R>::type acc[FM][FN];
+  f32x4 acc[FM][FN];
   auto clear = [&] {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int e = 0; e < R * R / 64; ++e) acc[i][j][e] = 0.0f;
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   };
-  // fragment e: channels for e % F < FN, activation rows after; row R e' + r of this wave's part
-  // ((row >> 1) & 7 does not depend on e'), block H h + q (h = e / F) of the stage, chunk 4 s + that of the pair's
-  // stage s.  Scales likewise: byte H h + q of each stage's dword.
+  // fragment e: channels for e < FN, activation rows after; row 16 e' + r of this wave's
+  // part ((row >> 1) & 7 does not depend on e'), chunk 4 h + q of the pair's stage h
   const uint32_t swz = (uint32_t)((q ^ ((r >> 1) & 7)) * 16);
-  const uint32_t xfrag = (uint32_t)((wm * FM * R + r) * 128) + swz;
-  const uint32_t wfrag = (uint32_t)((BM + wn * FN * R + r) * 128) + swz;
-  const uint32_t xsrow = (uint32_t)(kScales + (wm * FM * R + r) * 64);
-  const uint32_t wsrow = (uint32_t)(kScales + (BM + wn * FN * R + r) * 64);
-  uint32_t sel[H];
-#pragma unroll
-  for (int g = 0; g < H; ++g) sel[g] = (uint32_t)((2 * g + q) | ((2 * g + q + 4) << 8)) | 0x0C0C0000u;
+  const uint32_t xfrag = (uint32_t)((wm * FM * 16 + r) * 128) + swz;
+  const uint32_t wfrag = (uint32_t)((BM + wn * FN * 16 + r) * 128) + swz;
+  const uint32_t xsrow = (uint32_t)(kScales + (wm * FM * 16 + r) * 64);
+  const uint32_t wsrow = (uint32_t)(kScales + (BM + wn * FN * 16 + r) * 64);
+  const uint32_t sel = (uint32_t)(q | ((q + 4) << 8)) | 0x0C0C0000u;
 
-  u32x4 f[2][F * H];                            // fragments of this stage and the next
-  uint32_t sc[F * H], scn[F * H];               // packed scale bytes of four stages, and the next four
+  u32x4 f[2][F];                                // fragments of this stage and the next
+  uint32_t sc[F], scn[F];                       // packed scale bytes of four stages, and the next four
   auto read = [&](int buf, int j4, int e) {     // stage j4 of four: slot j4 / 2, half j4 % 2
-    const uint32_t x = (uint32_t)(64 * (j4 & 1) + 32 * (e / F));
-    const uint32_t o = e % F < FN ? (wfrag ^ x) + (e % F) * (R * 128) : (xfrag ^ x) + (e % F - FN) * (R * 128);
+    const uint32_t o = e < FN ? (wfrag ^ (uint32_t)(64 * (j4 & 1))) + e * 2048
+                              : (xfrag ^ (uint32_t)(64 * (j4 & 1))) + (e - FN) * 2048;
     f[buf][e] = *reinterpret_cast<const u32x4*>(smem + (j4 >> 1) * kSlot + o);
   };
   auto read_scales = [&](int group, int e) {
-    const uint32_t o = e < FN ? wsrow + e * (R * 64) : xsrow + (e - FN) * (R * 64);
+    const uint32_t o = e < FN ? wsrow + e * 1024 : xsrow + (e - FN) * 1024;
     return *reinterpret_cast<const u32x4*>(smem + o + (uint32_t)(((group & 3) ^ ((r >> 2) & 3)) * 16));
-  };
-  auto pack_scales = [&](uint32_t (&to)[F * H], u32x4 raw, int e, int shift) {
-#pragma unroll
-    for (int g = 0; g < H; ++g) to[e + g * F] = pack_bytes(raw, sel[g]) >> shift;
   };
   auto shift_of = [&](int group) { return 8 * min(3, kt0 + 4 * group - group_start(group)); };
 
@@ -325,22 +278,19 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
     if constexpr (cur == 1) {
       wait_vmcnt<0>();
       mx_barrier();
-      if (!(J == 1 && ahead)) next_pair();      // the next tile starts with its first pair
     }
-    if (stage == ragged) {
+    const int pair = (stage >> 1) + (cur == 1 ? 2 : 1);
+    const Src src = source(ahead ? pair - (n_stages >> 1) : pair);
+    if (rem != 0 && kt0 + stage == KT - 1 && q >= rem) {
 #pragma unroll
-      for (int g = 0; g < H; ++g)
-        if (2 * g + q >= rem) {
-#pragma unroll
-          for (int j = 0; j < FN; ++j) f[cur][j + g * F] = u32x4{0, 0, 0, 0};
-        }
+      for (int j = 0; j < FN; ++j) f[cur][j] = u32x4{0, 0, 0, 0};
     }
     // Between the matrix instructions: a copy every kEvery of them, from the second step of
     // a pair on into the first step of the next (in a burst they would fill the memory
     // pipeline and hold back the wave's matrix instructions); reads one each.
     constexpr int kLag = 3;                     // a scale read is packed three operations later
     constexpr int kCopies = C + 1;              // the pair's, and every other pair scales
-    constexpr int kReads = F * H + (J == 3 ? F + kLag : 0);
+    constexpr int kReads = F + (J == 3 ? F + kLag : 0);
     constexpr int kPer = (kReads + T - 1) / T;  // more than one where the tile is small
     u32x4 raw[F];
     const int group = ahead ? 0 : (stage + 1) >> 2, shift = J == 3 ? shift_of(group) : 0;
@@ -352,60 +302,55 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
         constexpr int slot = cur == 1 ? J >> 1 : (J >> 1) ^ 1;
         // the last group of the scales in LDS is in registers by now
         if (u == 0) { if (J == 1 && (ahead || ((stage + 3) & 15) == 0)) copy_scales(ahead ? 0 : (stage + 3) >> 4); }
-        else copy(slot, u - 1);
+        else copy(src, slot, u - 1);
       }
 #pragma unroll
       for (int o = t * kPer; o < (t + 1) * kPer; ++o) {
-        if (o < F * H) {
+        if (o < F) {
           read(nxt, (J + 1) % 4, o);
         } else if (o < kReads) {
-          const int e = o - F * H;
-          if (e >= kLag) pack_scales(scn, raw[e - kLag], e - kLag, shift);
+          const int e = o - F;
+          if (e >= kLag) scn[e - kLag] = pack_bytes(raw[e - kLag], sel) >> shift;
           if (e < F) raw[e] = read_scales(group, e);
         }
       }
-      const int i = t / FN % FM, j = t % FN, w = t / (FM * FN) * F + j, x = t / (FM * FN) * F + FN + i;
-      if constexpr (R == 16)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(f[cur][w]), mx_operand(f[cur][x]),
-                                                                    acc[i][j], 4, 4, J, (int)sc[w], J, (int)sc[x]);
-      else
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(f[cur][w]), mx_operand(f[cur][x]),
-                                                                   acc[i][j], 4, 4, J, (int)sc[w], J, (int)sc[x]);
+      const int i = t / FN, j = t % FN;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(f[cur][j]), mx_operand(f[cur][FN + i]),
+                                                                  acc[i][j], 4, 4, J, (int)sc[j], J, (int)sc[FN + i]);
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (J == 3) {
 #pragma unroll
-      for (int e = 0; e < F * H; ++e) sc[e] = scn[e];
+      for (int e = 0; e < F; ++e) sc[e] = scn[e];
     }
-    // no instruction: keeps the compiler from moving this step's products behind the branches of a later one
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) asm volatile("" : "+a"(acc[i][j]));
   };
 
   constexpr int kEarly = (T - 1) / kEvery < C ? (T - 1) / kEvery : C;
   int tile = blockIdx.x;
   copy_scales(0);
+  {
+    const Src p0 = source(0), p1 = source(1);
 #pragma unroll
-  for (int u = 0; u < C; ++u) copy(0, u);
-  // of pair 1 the copies that a second step would have issued; the first step issues the rest
-  next_pair();
+    for (int u = 0; u < C; ++u) copy(p0, 0, u);
+    // of pair 1 the copies that a second step would have issued; the first step issues the rest
 #pragma unroll
-  for (int u = 0; u < kEarly; ++u) copy(1, u);
+    for (int u = 0; u < kEarly; ++u) copy(p1, 1, u);
+  }
   wait_vmcnt<kEarly>();
   mx_barrier();
 #pragma unroll
-  for (int e = 0; e < F * H; ++e) read(0, 0, e);
-#pragma unroll
-  for (int e = 0; e < F; ++e) pack_scales(sc, read_scales(0, e), e, shift_of(0));
+  for (int e = 0; e < F; ++e) {
+    read(0, 0, e);
+    sc[e] = pack_bytes(read_scales(0, e), sel) >> shift_of(0);
+  }
   for (;;) {
     const int next = tile + (int)gridDim.x;
     const bool more = CHAIN && next < a.tiles;
-    const int m = m0 + wm * FM * R, n = n0 + wn * FN * R;
+    const int m = m0 + wm * FM * 16, n = n0 + wn * FN * 16;
     clear();
     for (int s = 0; s < n_stages; s += 4) {
       const bool ahead = more && s + 4 >= n_stages;
+      // the conditions also keep the compiler from moving a step's products into a later one
       step(std::integral_constant<int, 0>{}, s, false);
       if (ahead) set_tile(next);
       if (s + 1 < n_stages) step(std::integral_constant<int, 1>{}, s, ahead);
@@ -416,7 +361,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
       wait_vmcnt<0>();
       lds_barrier();                            // no copy and no read of the slots is left
     }
-    mx_store_tile<R, !CHAIN>(a, acc, m, n, smem + kOut + wave * kMxStage<BN / 2>);
+    mx_store_tile<FM, FN, !CHAIN>(a, acc, m, n, smem + kOut + wave * kMxStage<FN>);
     if (!more) break;
     tile = next;
   }
@@ -617,7 +562,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a16_kernel(MxTileArgs a) {
   }
   wait_vmcnt<0>();
   lds_barrier();                                // no copy and no read of the slots is left
-  mx_store_tile<16, true>(a, acc, m0 + wm * FM * 16, n0 + wn * FN * 16, smem + wave * kMxStage<FN * 16>);
+  mx_store_tile<FM, FN, true>(a, acc, m0 + wm * FM * 16, n0 + wn * FN * 16, smem + wave * kMxStage<FN>);
 }
 
 }  // namespace w4
