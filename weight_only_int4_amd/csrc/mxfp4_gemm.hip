@@ -35,8 +35,8 @@ constexpr MxTile kTiles4[] = {{256, 256, 1, 7.0f, 0.87f, 0.87f}, {256, 192, 1, 5
 constexpr MxTile kTiles16[] = {{256, 192, 1, 6.0f, 2.48f, 2.48f}, {128, 128, 1, 3.2f, 0.88f, 0.97f},
                                {128, 64, 2, 2.4f, 0.62f, 1.03f}, {64, 64, 3, 1.7f, 0.50f, 1.16f}};
 constexpr int kCus = 256;
-// More than one round of the 256 x 192 tile is chained where K allows it: a further tile starts so much sooner.
-// (A single round keeps the other form, 41.3 against 42.3 us at K = 6144.)
+// More than one round of the 256 x 192 tile is chained where K allows it: a further tile starts so many
+// microseconds sooner.  (A single round keeps the other form, 41.0 us against 42.0 at K = 6144.)
 constexpr int kChained = 1;
 constexpr double kChainGain = 1.5;
 

@@ -13,7 +13,9 @@
 // tile's side.  What two waves would overlap, the single one overlaps itself: between its
 // matrix instructions it reads the next stage's fragments and issues copies.  Measured at
 // M = 2048, K = 5120, N = 17408, 4-bit: eight waves in one phase 179 us, two waves per SIMD in
-// opposite phases 152, this 106 (3.4 PFLOP/s; the matrix instructions alone, on random data, 56).
+// opposite phases 152, this 104 (3.5 PFLOP/s; 87 on zeros, so part of it is power; the matrix
+// instructions alone, on random data, 56).  Not LDS or the copies: without either the loop takes
+// as long, and the next stage's reads hide behind the matrix instructions.
 //
 // LDS layout: position p of a row holds its 16-byte chunk p ^ f(row), with f chosen for each
 // row length so that every pass of a fragment read covers all 64 banks once (measured with
@@ -136,8 +138,9 @@ __device__ __forceinline__ void mx_store_tile(const MxTileArgs& a, const f32x4 (
 // MXFP4 activations.  Four waves (2 x 2), one per SIMD, BM / 2 rows x BN / 2 channels each.
 // CHAIN: a workgroup takes the tiles blockIdx.x + i gridDim.x in turn, and the copies run on from one tile
 // to the next, so that a tile's outputs are stored while the next one's first stages arrive
-// (needs stages in fours, and M >= BM and N >= BN).  M = 2048, K = 2048, N = 17408: 47.3 us against 50.4;
-// K = 5120: 105.5 against 107.5, which is the power limit (88 on zeros); K = 1536, N = 17401: 40.9 against 47.8.
+// (needs stages in fours, and M >= BM and N >= BN).  Inputs from memory, M = 2048, N = 17408: K = 2048
+// 56.7 us against 58.6, K = 5120 113.5 against 121.7; N = 17401: 116 against 127; M = 4096, K = 5120, N = 17408:
+// 207 against 223.
 template <int BM, int BN, bool CHAIN>
 __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
   constexpr int W = 4;                          // waves
