@@ -1,7 +1,8 @@
 /*
  * w4a16.h -- weight-only int4, group-128 quantized linear layers (W4A16) on
  * AMD CDNA4 (MI355X, gfx950): quantize + pack, decode GEMV, prefill GEMM and the
- * batched fake-quant loss of an AWQ scale-exponent / clip-shrink search.
+ * batched fake-quant loss of an AWQ scale-exponent / clip-shrink search; and linears in
+ * MXFP4 (4-bit microscaling floats).
  *
  * Sources for what is computed (web pages, cited by title and section):
  *   [AWQ-W4 card]  model card "rebuttal_w4g128_awq_w2": details table rows

@@ -1,4 +1,4 @@
-"""Weight-only int4, group-128 linear layers (W4A16) on AMD MI355X (gfx950).
+"""Weight-only int4, group-128 linear layers (W4A16), and MXFP4 ones, on AMD MI355X (gfx950).
 
 Thin Python binding over the C-ABI library ``libw4a16.so`` (see
 ``include/w4a16.h``).  The functions keep the C names; they check dtype,
@@ -8,7 +8,8 @@ non-zero status.  Every computation runs in the library's HIP kernels: there
 is no Python or CPU fallback, and a missing library is an error.
 
 Tensor conventions: bf16 data as ``torch.bfloat16``; packed uint32 words
-(qweight, qzeros) as ``torch.int32`` tensors holding the same bits.
+(qweight, qzeros, MXFP4 codes) as ``torch.int32`` tensors holding the same bits; MXFP4
+scale bytes as ``torch.uint8``.
 """
 from __future__ import annotations
 
