@@ -33,6 +33,7 @@
 // relied on to be part of the check: a tile that would end past the last row moves back to
 // end there, and has some outputs (the same bits) in common with the tile before.
 #include <algorithm>
+#include <cfloat>
 
 #include "mxfp4.hpp"
 
@@ -264,10 +265,14 @@ int launch_stream(const MxStreamArgs& base, int waves, int splits, hipStream_t s
 
 template <int ACT, int SL, int RB>
 int launch_cols(const MxStreamArgs& a, const MxStreamPlan& p, hipStream_t stream) {
+  if constexpr (RB <= 2) {                      // more channel tiles than three need too many registers beyond
+    if (p.cols == 5) return launch_stream<ACT, SL, RB, 5>(a, p.waves, p.splits, stream);
+    if (p.cols == 4) return launch_stream<ACT, SL, RB, 4>(a, p.waves, p.splits, stream);
+  }
   switch (p.cols) {
     case 1: return launch_stream<ACT, SL, RB, 1>(a, p.waves, p.splits, stream);
     case 2: return launch_stream<ACT, SL, RB, 2>(a, p.waves, p.splits, stream);
-    default: return launch_stream<ACT, SL, RB, 4>(a, p.waves, p.splits, stream);
+    default: return launch_stream<ACT, SL, RB, 3>(a, p.waves, p.splits, stream);
   }
 }
 
@@ -291,38 +296,49 @@ int launch_act(const MxStreamArgs& a, const MxStreamPlan& p, hipStream_t stream)
 
 }  // namespace
 
-// Rules from a sweep of every form over hidden-2048 and 27B-shaped linears, 1 to 64 rows
+// Rules from a sweep of every plan over hidden-2048 to 27B-shaped linears, 1 to 333 rows
 // (microseconds, chosen against the other side):
-//  * Slices: 4 up to 4 rows, 2 up to 8.  For 9 to 16 rows (24 with bf16 activations) two
-//    slices pay where rows of weights are long: K = 6144, N = 2048, 16 rows 5.9 against 6.5,
-//    K = 5120, N = 17408 16.5 against 18; at K = 2048 one slice with bf16 activations, 3.7
-//    against 4.1.
-//  * Channel tiles per workgroup: more of them share the activations, fewer fill the
-//    CUs.  M = 16: 640 tiles 18.5 with four against 21.8 with two, 384 tiles 4.6 with two against
-//    5.3 with one, 256 tiles 5.9 with one against 6.6 with two.  From 25 rows on two (registers).
-//  * Waves: with few workgroups the waves split K four ways; many workgroups need none of it
-//    (K = 5120, N = 17408: M = 1 10.2 with one against 11.4 with four, M = 16 15.3 against 17.0 with
-//    two).
-//  * K is split over workgroups, with a second launch, where few tiles meet a long K: M = 37,
-//    K = 6144, N = 2048 9.1 against 10.7.
+//  * Slices: 4 up to 4 rows, 2 up to 8, and up to 24 with 4-bit activations or long rows of weights: bf16, 16
+//    rows, K = 5120, N = 17408 13.3 against 16.0 with one slice, K = 2048, N = 6144 5.1 against 4.7; 4 bits, 24
+//    rows, K = N = 2048 4.7 against 5.4.  Their use is the piece of a row that one load takes (one
+//    row, K = 5120, N = 17408: 64 bytes 19.4, 128 bytes 11.5, 256 bytes 9.95).
+//  * Channel tiles per workgroup: what the busiest CU has to fetch decides, its workgroups' weights, past the
+//    L2, at 39 bytes per nanosecond (half that in 64-byte pieces), and their activations at 100.  K = 5120,
+//    N = 17408, 16 rows: three tiles (726 workgroups, three on a CU) 13.3, four (544, three) 14.9, two
+//    (1088, five) 17.4, one (nine) 23; 4 bits five tiles 11.8, four 13.7, two 14.5; K = 17408, N = 5120, 16 rows:
+//    three 15.7, four 18.0.  Beyond two row tiles, and with two slices of bf16 activations, five lack
+//    registers or waves (K = 5120, N = 17408, 16 rows: 14.9 to 16.3).
+//  * Above 24 rows a long K may be split over workgroups, with a second launch: M = 37, K = 6144, N = 2048 9.1
+//    against 10.7, M = 32, K = 17408, N = 5120 20.4 against 28.
+//  * Waves, which share K: about one for each SIMD and, with 4-bit activations, two (bf16, 726 workgroups 13.3 with
+//    one, 14.5 with two; 214 workgroups 15.7 with four, 18.7 with two; 4 bits, 726: 12.1 with four, 15.7 with one).
 MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N) {
+  constexpr int kCus = 256;
   MxStreamPlan p{};
-  p.slices = M <= 4 ? 4 : M <= 8 ? 2 : act_bits == 4 ? (M <= 16 ? 2 : 1) : (M <= 24 && K >= 4096 ? 2 : 1);
+  p.slices = M <= 4 ? 4 : M <= 8 || (M <= 24 && (act_bits == 4 || K >= 4096)) ? 2 : 1;
   p.rows = std::min(4, (M * p.slices + 15) / 16);
   const int ch = 16 / p.slices;                 // channels per tile, and activation rows per tile
   const int steps = (K / kMxBlock + 4 * p.slices - 1) / (4 * p.slices);
-  const long long tiles = (N + ch - 1LL) / ch * ((M + (long long)ch * p.rows - 1) / (ch * p.rows));
-  if (M <= 4) p.cols = tiles >= 512 ? 2 : 1;
-  else if (M <= 8) p.cols = tiles >= 2048 ? 2 : tiles >= 512 ? 4 : 1;
-  else if (M <= 24) p.cols = tiles >= 512 ? 4 : tiles >= 320 ? 2 : 1;
-  else p.cols = tiles >= 320 ? 2 : 1;
-  p.splits = 1;
-  if (M > 24 && steps >= 32 && tiles <= 256) {
-    p.cols = 2;
-    p.splits = 4;
-  }
-  const long long wgs = (tiles + p.cols - 1) / p.cols * p.splits;
-  p.waves = wgs <= 512 ? 4 : wgs <= 1280 && M <= 8 ? 2 : 1;
+  const long long row_groups = (M + (long long)ch * p.rows - 1) / (ch * p.rows);
+  // microseconds of a workgroup: per channel tile, and for the activations and its start
+  const double weights = ch * 0.53e-3 * K / (p.slices == 1 ? 20.0 : 39.0);
+  const double activations = std::min(M, ch * p.rows) * (act_bits == 16 ? 2.0e-3 : 0.53e-3) * K / 100.0;
+  const int most = p.rows > 2 ? 3 : act_bits == 16 && p.slices == 2 ? 4 : 5;
+  double best = DBL_MAX;
+  long long wgs = 0;
+  for (int splits = 1; splits <= (M > 24 && steps >= 32 ? 4 : 1); splits *= 4)
+    for (int cols = 1; cols <= most; ++cols) {
+      const long long n = (N + (long long)ch * cols - 1) / (ch * cols) * row_groups * splits;
+      double us = (double)((n + kCus - 1) / kCus) * ((cols * weights + activations) / splits + 0.2);
+      if (splits > 1) us += 2.5 + splits * 2.7e-6 * M * N;
+      if (us < best) {
+        best = us;
+        p.cols = cols;
+        p.splits = splits;
+        wgs = n;
+      }
+    }
+  p.waves = act_bits == 16 ? (wgs <= 300 ? 4 : wgs <= 640 ? 2 : 1) : (wgs <= 768 ? 4 : wgs <= 1100 ? 2 : 1);
   while (p.waves > 1 && 2 * p.waves * p.splits > steps) p.waves /= 2;   // two steps a wave at least
   return p;
 }
@@ -342,8 +358,8 @@ int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t str
 }
 
 // The tiled form with 4-bit activations from 17 rows on (K = 2048, N = 6144: M = 20 5.4 against 5.8,
-// M = 64 5.6 against 9.0), 33 on small weights (K = N = 2048, M = 20: 5.3 against 4.8), 9 on large
-// ones (K = 5120, N = 17408, M = 9 13.2 against 16.9, M = 16 14.3 against 17.0); with bf16
+// M = 64 5.6 against 9.0; K = 5120, N = 17408: M = 16 14.3 against 11.8, M = 32 14.6 against 23), 33 on small weights
+// (K = N = 2048, M = 20: 5.3 against 4.8); with bf16
 // ones where more than 32 rows and 10^9 products meet (K = 2048, N = 6144: M = 64 11.1 against
 // 9.0, M = 128 12.3 against 15.9; K = 5120, N = 17408: M = 32 29 against 24, M = 64 33 against 35).
 // Where scale rows have to be padded first, by another launch, it has to be worth that
@@ -353,7 +369,7 @@ bool mxfp4_use_tile(int act_bits, int M, int K, int N) {
   if (act_bits == 16) return M > 32 && MNK >= 1e9;
   const int KB = K / kMxBlock;
   if (KB % 4 != 0 || KB < 16) return MNK >= 2e9;
-  return M > (NK >= 6e7 ? 8 : NK >= 8e6 ? 16 : 32);
+  return M > (NK >= 8e6 ? 16 : 32);
 }
 
 MxPlan plan_mxfp4_gemm(int act_bits, int M, int K, int N) {
