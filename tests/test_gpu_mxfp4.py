@@ -233,6 +233,18 @@ def test_product_tiled(M, K, N, act):
     assert torch.equal(Y, again)
 
 
+# Shapes of the register form on which a workgroup has one to five tiles of 4, 8 or 16 channels, with the last
+# workgroup's moved back; K that ends inside a step; K split over workgroups.
+STREAM = [(1, 5120, 17411), (3, 2080, 6151), (4, 1536, 9001), (7, 2048, 6145), (13, 5152, 17399), (16, 4096, 12289),
+          (21, 4128, 12289), (32, 17408, 5121), (30, 5120, 17403), (27, 8224, 1025), (37, 6176, 2047), (17, 2048, 2049)]
+
+
+@pytest.mark.parametrize("act", [16, 4])
+@pytest.mark.parametrize("M,K,N", STREAM)
+def test_product_stream(M, K, N, act):
+    test_product_tiled(M, K, N, act)
+
+
 @pytest.mark.parametrize("act", [16, 4])
 @pytest.mark.parametrize("M,K,N", [(520, 2080, 1001), (257, 4160, 1000), (40, 17408, 1500), (2047, 2048, 3000), (2047, 2016, 17401), (940, 6752, 13941)])
 def test_product_tiled_special_values(M, K, N, act):

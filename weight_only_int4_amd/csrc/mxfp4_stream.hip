@@ -25,9 +25,9 @@
 // turned into operand order through 4 KB of LDS per wave: in operand order a load would be
 // 64 pieces of 16 bytes, four times the cache lines.  Chunk k of column c is at position k ^
 // mx_swizzle16(c), so that both sides are free of bank conflicts.
-// Measured: M = 1, K = 5120, N = 17408 10.0 us, 4.8 TB/s of weights (a large copy reaches 4.9); M = 16
-// 14.9 with bf16 activations, where a wave's expansion, turning and matrix instructions follow one
-// another and more waves only add activations to load; M = 1, K = N = 2048 2.8, an empty kernel 2.5.
+// Measured: M = 1, K = 5120, N = 17408 9.7 us, 4.9 TB/s of weights, what a large copy reaches; M = 16
+// 13.3 with bf16 activations and 11.8 with 4-bit ones, bound by what the busiest CU fetches (three
+// workgroups, where 2.8 would be even); M = 1, K = N = 2048 2.8, an empty kernel 2.5.
 // Loads are range-checked buffer loads: rows past M and N and blocks past K read
 // zeros and touch no memory.  A tile's first row is the scalar offset of the loads, which is not
 // relied on to be part of the check: a tile that would end past the last row moves back to
