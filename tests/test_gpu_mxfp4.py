@@ -508,3 +508,26 @@ def test_convert_mxfp4_checkpoint(tmp_path):
             assert np.array_equal(out[sn].numpy(), byte), name
         else:
             assert np.array_equal(out[name].view(torch.int16).numpy().view(np.uint16), W), name
+
+
+@pytest.mark.parametrize("act", [16, 4])
+def test_two_streams_at_once(act):
+    """Calls on two streams with workspaces of their own do not disturb each other."""
+    say("mx product two streams", act)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    cases = []
+    for M, K, N in ((37, 6176, 2047), (300, 17440, 255)):
+        qw, sw, _ = _random_packed(gen, N, K)
+        acts = (torch.randn(M, K, generator=gen, device="cuda").bfloat16(),) if act == 16 else _random_packed(gen, M, K)[:2]
+        want = _product(act, acts, qw, sw)
+        Y = torch.empty_like(want)
+        make = w4.mxfp4_a16_gemm_launcher if act == 16 else w4.mxfp4_a4_gemm_launcher
+        cases.append((make(*acts, qw, sw, Y), Y, want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for launch, _, _, stream in cases:
+            with torch.cuda.stream(stream):
+                launch()
+    torch.cuda.synchronize()
+    for _, Y, want, _ in cases:
+        assert torch.equal(Y, want)

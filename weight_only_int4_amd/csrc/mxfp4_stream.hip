@@ -357,16 +357,17 @@ int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t str
   return launch_split_reduce(a.partial, p.splits, MN, MN, g.Y, stream);
 }
 
-// The tiled form with 4-bit activations from 17 rows on (K = 2048, N = 6144: M = 20 5.4 against 5.8,
-// M = 64 5.6 against 9.0; K = 5120, N = 17408: M = 16 14.3 against 11.8, M = 32 14.6 against 23), 33 on small weights
-// (K = N = 2048, M = 20: 5.3 against 4.8); with bf16
-// ones where more than 32 rows and 10^9 products meet (K = 2048, N = 6144: M = 64 11.1 against
-// 9.0, M = 128 12.3 against 15.9; K = 5120, N = 17408: M = 32 29 against 24, M = 64 33 against 35).
-// Where scale rows have to be padded first, by another launch, it has to be worth that
-// (4-bit, M = 333, K = 1056, N = 2047: 7.8 here against 9.5).
+// The tiled form (stream against tile, microseconds): with 4-bit activations from 17 rows on (K = 2048, N = 6144:
+// M = 20 5.8 against 5.4, M = 64 9.3 against 5.4; K = 5120, N = 17408: M = 16 11.8 against 14.3, M = 32 19.9 against 15.9),
+// 33 on small weights (K = N = 2048: M = 20 4.9 against 5.4, M = 40 6.8 against 5.4).  With bf16 ones, whose
+// expansion it shares among fewer rows, from 129 rows on and 10^9 products (K = 2048, N = 6144: M = 128 11.3 against
+// 12.5, M = 200 16.5 against 14.3; K = 5120, N = 5120: 19.6 against 26.0, 32.9 against 31.2), 65 on wide weights
+// (K = 5120, N = 17408: M = 64 32.3 against 33.2, M = 96 46.5 against 41.1; K = 1536, N = 9000: 9.5 against 9.6,
+// 14.1 against 11.1).  Where scale rows have to be padded first, by another launch, it has to be
+// worth that (4-bit, M = 333, K = 1056, N = 2047: 7.2 against 9.5).
 bool mxfp4_use_tile(int act_bits, int M, int K, int N) {
   const double NK = (double)N * K, MNK = M * NK;
-  if (act_bits == 16) return M > 32 && MNK >= 1e9;
+  if (act_bits == 16) return MNK >= 1e9 && M > (N >= 8192 ? 64 : 128);
   const int KB = K / kMxBlock;
   if (KB % 4 != 0 || KB < 16) return MNK >= 2e9;
   return M > (NK >= 8e6 ? 16 : 32);
