@@ -339,7 +339,9 @@ MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N) {
       }
     }
   p.waves = act_bits == 16 ? (wgs <= 300 ? 4 : wgs <= 640 ? 2 : 1) : (wgs <= 768 ? 4 : wgs <= 1100 ? 2 : 1);
-  while (p.waves > 1 && 2 * p.waves * p.splits > steps) p.waves /= 2;   // two steps a wave at least
+  // two (four slices) or two and a half steps a wave at least (4 bits, M = 333, K = 1056, N = 2047: 6.7 with two waves,
+  // 7.2 with four)
+  while (p.waves > 1 && (p.slices == 4 ? 4 : 5) * p.waves * p.splits > 2 * steps) p.waves /= 2;
   return p;
 }
 
@@ -364,7 +366,7 @@ int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t str
 // 12.5, M = 200 16.5 against 14.3; K = 5120, N = 5120: 19.6 against 26.0, 32.9 against 31.2), 65 on wide weights
 // (K = 5120, N = 17408: M = 64 32.3 against 33.2, M = 96 46.5 against 41.1; K = 1536, N = 9000: 9.5 against 9.6,
 // 14.1 against 11.1).  Where scale rows have to be padded first, by another launch, it has to be
-// worth that (4-bit, M = 333, K = 1056, N = 2047: 7.2 against 9.5).
+// worth that (4-bit, M = 333, K = 1056, N = 2047: 6.7 against 9.5).
 bool mxfp4_use_tile(int act_bits, int M, int K, int N) {
   const double NK = (double)N * K, MNK = M * NK;
   if (act_bits == 16) return MNK >= 1e9 && M > (N >= 8192 ? 64 : 128);
