@@ -192,3 +192,49 @@ def test_converter_selects_by_block():
 def test_converter_refuses_unknown_format(tmp_path):
     with pytest.raises(ValueError, match="format"):
         C.convert_checkpoint(str(tmp_path), str(tmp_path / "out"), fmt="int3")
+
+
+# ---------------------------------------------------------------- the binding's own checks
+
+class _OnGpu(torch.Tensor):
+    """A tensor without storage that the binding takes for one on a GPU."""
+    is_cuda = True
+
+
+def _huge(shape, dtype):
+    return torch.empty(shape, dtype=dtype, device="meta").as_subclass(_OnGpu)
+
+
+def _no_call(*args):
+    raise AssertionError("the library was called")
+
+
+@pytest.fixture
+def no_library_call(monkeypatch):
+    """Any call that gets past the checks fails the test."""
+    monkeypatch.setattr(w4, "_mx_call", _no_call)
+    monkeypatch.setattr(w4, "_workspace", _no_call)
+
+
+_BIG = 2 ** 32            # as a C int: 0, so 2^32 + 32 would pass for 32
+
+
+def test_binding_refuses_sizes_past_an_int(no_library_call):
+    """Sizes are int in the C interface; a larger one would lose its upper bits on the way."""
+    i32, u8, bf16 = torch.int32, torch.uint8, torch.bfloat16
+    for rows, K in ((1, _BIG + 32), (1, 2 ** 31), (_BIG + 4, 32), (2 ** 31, 32)):
+        with pytest.raises(ValueError, match="2147483647"):
+            w4.mxfp4_quantize(_huge((rows, K), bf16))
+        with pytest.raises(ValueError, match="2147483647"):
+            w4.mxfp4_dequantize(_huge((rows, K // 8), i32), _huge((rows, K // 32), u8))
+        small_q, small_s = _huge((4, K // 8), i32), _huge((4, K // 32), u8)
+        with pytest.raises(ValueError, match="2147483647"):
+            w4.mxfp4_a16_gemm(_huge((rows, K), bf16), small_q, small_s)
+        with pytest.raises(ValueError, match="2147483647"):
+            w4.mxfp4_a4_gemm(_huge((rows, K // 8), i32), _huge((rows, K // 32), u8), small_q, small_s)
+    for N in (_BIG + 4, 2 ** 31):
+        q, s = _huge((N, 8), i32), _huge((N, 2), u8)
+        with pytest.raises(ValueError, match="2147483647"):
+            w4.mxfp4_a16_gemm(_huge((1, 64), bf16), q, s)
+        with pytest.raises(ValueError, match="2147483647"):
+            w4.mxfp4_a4_gemm(_huge((1, 8), i32), _huge((1, 2), u8), q, s)

@@ -605,12 +605,17 @@ def _mx_call(fn, args, index):
         _check(rc)
 
 
-def _mx_width(t, per, name):
-    """K of a matrix stored with `per` channels per element of its rows."""
-    K = t.shape[1] * per
+_INT_MAX = 2 ** 31 - 1
+
+
+def _mx_sizes(t, per, name):
+    """(rows, K) of a matrix stored with `per` channels per element of its rows."""
+    rows, K = t.shape[0], t.shape[1] * per
     if K == 0 or K % MX_BLOCK:
         raise ValueError(f"{name}: K must be a positive multiple of {MX_BLOCK}, got {K}")
-    return K
+    if rows > _INT_MAX or K > _INT_MAX:       # ctypes would keep the low 32 bits
+        raise ValueError(f"{name}: rows and K must be at most {_INT_MAX}, got {rows} and {K}")
+    return rows, K
 
 
 def mxfp4_quantize(W, s=None, codes=None, scales=None):
@@ -620,7 +625,7 @@ def mxfp4_quantize(W, s=None, codes=None, scales=None):
     lib = load_library()
     _need(W, torch.bfloat16, "W", 2)
     dev = W.device
-    N, K = W.shape[0], _mx_width(W, 1, "W")
+    N, K = _mx_sizes(W, 1, "W")
     if s is not None:
         _mx_need(s, torch.float32, "s", (K,), dev)
     if codes is None:
@@ -641,7 +646,7 @@ def mxfp4_dequantize(codes, scales, W=None):
     lib = load_library()
     _need(codes, torch.int32, "codes", 2)
     dev = codes.device
-    N, K = codes.shape[0], _mx_width(codes, 8, "codes")
+    N, K = _mx_sizes(codes, 8, "codes")
     _mx_need(scales, torch.uint8, "scales", (N, K // MX_BLOCK), dev)
     if W is None:
         W = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
@@ -656,13 +661,13 @@ def _mx_gemm_launcher(cname, acts, qweight, scales, Y, workspace):
     lib = load_library()
     if len(acts) == 1:
         _need(acts[0], torch.bfloat16, "X", 2)
-        dev, M, K = acts[0].device, acts[0].shape[0], _mx_width(acts[0], 1, "X")
+        dev, (M, K) = acts[0].device, _mx_sizes(acts[0], 1, "X")
     else:
         _need(acts[0], torch.int32, "Xq", 2)
-        dev, M, K = acts[0].device, acts[0].shape[0], _mx_width(acts[0], 8, "Xq")
+        dev, (M, K) = acts[0].device, _mx_sizes(acts[0], 8, "Xq")
         _mx_need(acts[1], torch.uint8, "xscales", (M, K // MX_BLOCK), dev)
     _need(qweight, torch.int32, "qweight", 2)
-    N = qweight.shape[0]
+    N = _mx_sizes(qweight, 8, "qweight")[0]
     _mx_need(qweight, torch.int32, "qweight", (N, K // 8), dev)
     _mx_need(scales, torch.uint8, "scales", (N, K // MX_BLOCK), dev)
     if Y is None:
