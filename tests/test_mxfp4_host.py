@@ -238,3 +238,38 @@ def test_binding_refuses_sizes_past_an_int(no_library_call):
             w4.mxfp4_a16_gemm(_huge((1, 64), bf16), q, s)
         with pytest.raises(ValueError, match="2147483647"):
             w4.mxfp4_a4_gemm(_huge((1, 8), i32), _huge((1, 2), u8), q, s)
+
+
+def test_binding_without_the_direct_device_calls(monkeypatch):
+    """A torch without the two direct calls takes the public ones."""
+    import importlib.util
+    monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    spec = importlib.util.spec_from_file_location("binding_without_direct_calls", w4.__file__)
+    binding = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(binding)
+
+    class Stream:
+        def __init__(self, index):
+            self.cuda_stream = 100 + index
+
+    entered = []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            entered.append(self.index)
+
+        def __exit__(self, *exc):
+            return False
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: Stream(index))
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    seen = []
+    for index in (1, 2):
+        binding._mx_call(lambda *args: seen.append(args) or 0, (7, 8), index)
+    assert seen == [(7, 8, 101), (7, 8, 102)]
+    assert entered == [2]                      # only for a device that is not the current one

@@ -589,9 +589,10 @@ def _mx_need(t, dtype, name, shape, device):
 
 
 # the calls behind torch.cuda.current_device() and current_stream().cuda_stream, without
-# the objects built around them (2 us of a 6 us launch)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the objects built around them (2 us of a 6 us launch); the public ones where torch lacks them
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_current_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                       or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 
 
 def _mx_call(fn, args, index):
