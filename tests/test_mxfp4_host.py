@@ -273,3 +273,13 @@ def test_binding_without_the_direct_device_calls(monkeypatch):
         binding._mx_call(lambda *args: seen.append(args) or 0, (7, 8), index)
     assert seen == [(7, 8, 101), (7, 8, 102)]
     assert entered == [2]                      # only for a device that is not the current one
+
+
+def test_few_rows_need_no_padded_scales(lib):
+    """Up to 24 rows a product does not copy a whole weight's scales first, whatever K (a size query of 0)."""
+    for name, f in _gemm_calls(lib):
+        for M in (1, 3, 4, 8, 16, 17, 24):
+            for K, N in ((2880, 201088), (2080, 151936), (5152, 400000), (480, 1000003), (17440, 65536)):
+                sz = ctypes.c_size_t(1)
+                assert f(M, K, N, x=None, xs=None, w=None, s=None, y=None, sz=ctypes.byref(sz)) == 0
+                assert sz.value == 0, (name, M, K, N)

@@ -365,13 +365,16 @@ int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t str
 // expansion it shares among fewer rows, from 129 rows on and 10^9 products (K = 2048, N = 6144: M = 128 11.3 against
 // 12.5, M = 200 16.5 against 14.3; K = 5120, N = 5120: 19.6 against 26.0, 32.9 against 31.2), 65 on wide weights
 // (K = 5120, N = 17408: M = 64 32.3 against 33.2, M = 96 46.5 against 41.1; K = 1536, N = 9000: 9.5 against 9.6,
-// 14.1 against 11.1).  Where scale rows have to be padded first, by another launch, it has to be
-// worth that (4-bit, M = 333, K = 1056, N = 2047: 6.7 against 9.5).
+// 14.1 against 11.1).  Where scale rows have to be padded first, by another launch, from 33 rows on and 2 10^9
+// products (4 bits, K = 2880, N = 201088: M = 4 65 against 110, M = 24 102 against 118, M = 33 132 against 121; K = 5152,
+// N = 20000: M = 24 27.4 against 32.6, M = 33 32.8 against 33.1, M = 64 39.4 against 36.7; K = 2080, N = 8192: M = 64 9.2
+// against 12.2, M = 128 12.5 against 13.2, M = 333 26.1 against 17.2; K = 1056, N = 8192: M = 128 7.6 against 8.3,
+// M = 333 14.1 against 10.6; K = 17440, N = 5120: M = 24 24.4 against 31.8, M = 33 32.0 against 33.0).
 bool mxfp4_use_tile(int act_bits, int M, int K, int N) {
   const double NK = (double)N * K, MNK = M * NK;
   if (act_bits == 16) return MNK >= 1e9 && M > (N >= 8192 ? 64 : 128);
   const int KB = K / kMxBlock;
-  if (KB % 4 != 0 || KB < 16) return MNK >= 2e9;
+  if (KB % 4 != 0 || KB < 16) return MNK >= 2e9 && M > 32;
   return M > (NK >= 8e6 ? 16 : 32);
 }
 
