@@ -265,10 +265,11 @@ int launch_stream(const MxStreamArgs& base, int waves, int splits, hipStream_t s
 
 template <int ACT, int SL, int RB>
 int launch_cols(const MxStreamArgs& a, const MxStreamPlan& p, hipStream_t stream) {
-  if constexpr (RB <= 2) {                      // more channel tiles than three need too many registers beyond
+  // what plan_mx_stream chooses from; the grid follows from the instance, so any would be right
+  if constexpr (RB <= 2 && !(ACT == 16 && SL == 2))
     if (p.cols == 5) return launch_stream<ACT, SL, RB, 5>(a, p.waves, p.splits, stream);
+  if constexpr (RB <= 2)
     if (p.cols == 4) return launch_stream<ACT, SL, RB, 4>(a, p.waves, p.splits, stream);
-  }
   switch (p.cols) {
     case 1: return launch_stream<ACT, SL, RB, 1>(a, p.waves, p.splits, stream);
     case 2: return launch_stream<ACT, SL, RB, 2>(a, p.waves, p.splits, stream);
@@ -286,8 +287,9 @@ int launch_act(const MxStreamArgs& a, const MxStreamPlan& p, hipStream_t stream)
       default: return launch_cols<ACT, 2, 3>(a, p, stream);
     }
   }
+  if constexpr (ACT == 16)                      // 4-bit activations: two slices up to 24 rows
+    if (p.rows == 1) return launch_cols<ACT, 1, 1>(a, p, stream);
   switch (p.rows) {
-    case 1: return launch_cols<ACT, 1, 1>(a, p, stream);
     case 2: return launch_cols<ACT, 1, 2>(a, p, stream);
     case 3: return launch_cols<ACT, 1, 3>(a, p, stream);
     default: return launch_cols<ACT, 1, 4>(a, p, stream);
