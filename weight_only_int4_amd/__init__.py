@@ -606,16 +606,14 @@ def _mx_call(fn, args, index):
         _check(rc)
 
 
-_INT_MAX = 2 ** 31 - 1
-
-
 def _mx_sizes(t, per, name):
     """(rows, K) of a matrix stored with `per` channels per element of its rows."""
-    rows, K = t.shape[0], t.shape[1] * per
+    rows, K = t.shape
+    K *= per
     if K == 0 or K % MX_BLOCK:
         raise ValueError(f"{name}: K must be a positive multiple of {MX_BLOCK}, got {K}")
-    if rows > _INT_MAX or K > _INT_MAX:       # ctypes would keep the low 32 bits
-        raise ValueError(f"{name}: rows and K must be at most {_INT_MAX}, got {rows} and {K}")
+    if (rows | K) >> 31:                      # ctypes would keep the low 32 bits
+        raise ValueError(f"{name}: rows and K must be at most {2 ** 31 - 1}, got {rows} and {K}")
     return rows, K
 
 
