@@ -7,11 +7,12 @@
 //
 // A block is four lanes of eight channels: 16-byte loads and 4-byte stores of
 // consecutive lanes are consecutive in memory, the maximum is two quad permutes, and
-// the rounding is the hardware's conversion (equal to the definition for every bf16
-// value and scale, checked exhaustively on the GPU).  A thread takes one chunk, no loop: bound by
+// the rounding is the hardware's conversion (equal to the definition in the tests: every
+// bf16 value at every scale, and fp32 values next to each border between magnitudes, at every
+// scale and below).  A thread takes one chunk, no loop: bound by
 // HBM traffic.  17408 x 5120 with s, 226 MB read and written: 38.6 us, 5.9 TB/s, from the caches where
-// the weight fits them (a large copy: 4.9 TB/s); the way back 32.4 us in the same state, 42.3 us (5.3 TB/s)
-// with inputs from memory.  16 x 2048 takes 2.2 us, as long as an empty kernel.
+// the weight fits them, 52.3 us (4.3 TB/s) from HBM (a large copy: 4.9 TB/s); the way back 32.4 and 42.7 us
+// (5.3 TB/s).  16 x 2048 takes 2.2 us, as long as an empty kernel.
 #include "mxfp4.hpp"
 
 #pragma clang fp contract(off)

@@ -158,6 +158,8 @@ int launch_mx_tile(const MxTilePlan& p, const MxGemmArgs& g, hipStream_t stream)
   }
   W4_CHECK_LAUNCH();
   if (p.splits > 1) {
+    // its rounding is for numbers; a NaN stays one where its low 16 bits are zero, as those that come of bf16
+    // NaNs and of NaN scales are (tested with every kind of bf16 NaN)
     const size_t MN = (size_t)g.M * g.N;
     return launch_split_reduce(a.partial, p.splits, MN, MN, g.Y, stream);
   }

@@ -8,14 +8,18 @@
 // the matrix instruction's row operand, so a lane ends with four consecutive channels
 // of one output row.
 //
-// One wave per SIMD, so that a tile is as large as the registers allow (256 x 256: 256 of
-// accumulators, the rest for fragments): the LDS traffic of a product falls with the
-// tile's side.  What two waves would overlap, the single one overlaps itself: between its
-// matrix instructions it reads the next stage's fragments and issues copies.  Measured at
-// M = 2048, K = 5120, N = 17408, 4-bit: eight waves in one phase 179 us, two waves per SIMD in
-// opposite phases 152, this 104 (3.5 PFLOP/s; 87 on zeros, so part of it is power; the matrix
-// instructions alone, on random data, 56).  Not LDS or the copies: without either the loop takes
-// as long, and the next stage's reads hide behind the matrix instructions.
+// One wave per SIMD, so that a tile is as large as the registers allow: the LDS traffic of a
+// product falls with the tile's side.  (256 x 192 takes 252 + 248 of the 512 registers; 256 x 256
+// all of them and 24 bytes a lane of scratch besides.)  What two waves would overlap, the
+// single one overlaps itself: between its matrix instructions it reads the next stage's
+// fragments and issues copies.  Measured at M = 2048, K = 5120, N = 17408, 4-bit: eight waves in
+// one phase 179 us, two waves per SIMD in opposite phases 152, this 104 to 112 (3.3 to 3.5 PFLOP/s).
+//
+// What bounds that: three rounds of 40 stages at 0.78 us (from K and N varied one at a time), 94 in
+// all, and 18 for three starts, the stores and the launch.  A stage's matrix instructions alone take
+// 0.51 us on random data; with inputs in the caches a stage takes 0.75, and 0.58 on zeros
+// (power); from memory 0.73 to 0.78 whatever the data, so there it is the copies' arrival.
+// The third round is 84 % full: 18432 channels, three full rounds, take 112 us, 17408 take 110.
 //
 // LDS layout: position p of a row holds its 16-byte chunk p ^ f(row), with f chosen for each
 // row length so that every pass of a fragment read covers all 64 banks once (measured with
@@ -375,7 +379,8 @@ __global__ __launch_bounds__(256, 1) void mx_tile_a4_kernel(MxTileArgs a) {
 // A stage of 128 channels is four steps of 32: step v multiplies word v of every MX block
 // (channels 8 v .. 8 v + 7 of it), expanded to bf16, with chunk 4 q + v of the
 // activation rows.  Two slots; a slot is free when the fragments of its last step are read.
-// M = 2048, K = 2048, N = 6144: 41 us, 1.25 PFLOP/s; the matrix instructions alone, on random
+// M = 2048, K = 2048, N = 6144: 40 to 44 us, 1.2 to 1.3 PFLOP/s: 16 stages of 2.0 us (1.9 on zeros), and
+// 12 for the start, the stores and the launch; the matrix instructions alone, on random
 // data, 31, and the expansion of the weights shares their issue slots.
 template <int BM, int BN>
 __global__ __launch_bounds__(256, 1) void mx_tile_a16_kernel(MxTileArgs a) {

@@ -25,9 +25,10 @@
 // turned into operand order through 4 KB of LDS per wave: in operand order a load would be
 // 64 pieces of 16 bytes, four times the cache lines.  Chunk k of column c is at position k ^
 // mx_swizzle16(c), so that both sides are free of bank conflicts.
-// Measured: M = 1, K = 5120, N = 17408 9.7 us, 4.9 TB/s of weights, what a large copy reaches; M = 16
-// 13.3 with bf16 activations and 11.8 with 4-bit ones, bound by what the busiest CU fetches (three
-// workgroups, where 2.8 would be even); M = 1, K = N = 2048 2.8, an empty kernel 2.5.
+// Measured, with four weights in turn (Infinity Cache; from HBM, 24 in turn): M = 1, K = 5120, N = 17408
+// 9.7 to 10.3 us (12.2 to 12.9, 3.7 to 3.9 TB/s of weights; a large copy reaches 4.9); M = 16 13.3 to 14.2 (18.6 to
+// 19.0) with bf16 activations and 11.8 to 12.3 (15.4) with 4-bit ones, bound by what the busiest CU
+// fetches (three workgroups, where 2.8 would be even); M = 1, K = N = 2048 2.8 (3.75), an empty kernel 2.5.
 // Loads are range-checked buffer loads: rows past M and N and blocks past K read
 // zeros and touch no memory.  A tile's first row is the scalar offset of the loads, which is not
 // relied on to be part of the check: a tile that would end past the last row moves back to
@@ -298,8 +299,8 @@ int launch_act(const MxStreamArgs& a, const MxStreamPlan& p, hipStream_t stream)
 
 }  // namespace
 
-// Rules from a sweep of every plan over hidden-2048 to 27B-shaped linears, 1 to 333 rows
-// (microseconds, chosen against the other side):
+// Rules from a sweep of every plan over hidden-2048 to 27B-shaped linears, 1 to 333 rows, a
+// few weights in turn, which the Infinity Cache holds (microseconds, chosen against the other side):
 //  * Slices: 4 up to 4 rows, 2 up to 8, and up to 24 with 4-bit activations or long rows of weights: bf16, 16
 //    rows, K = 5120, N = 17408 13.3 against 16.0 with one slice, K = 2048, N = 6144 5.1 against 4.7; 4 bits, 24
 //    rows, K = N = 2048 4.7 against 5.4.  Their use is the piece of a row that one load takes (one
@@ -341,8 +342,11 @@ MxStreamPlan plan_mx_stream(int act_bits, int M, int K, int N) {
       }
     }
   p.waves = act_bits == 16 ? (wgs <= 300 ? 4 : wgs <= 640 ? 2 : 1) : (wgs <= 768 ? 4 : wgs <= 1100 ? 2 : 1);
-  // two (four slices) or two and a half steps a wave at least (4 bits, M = 333, K = 1056, N = 2047: 6.7 with two waves,
-  // 7.2 with four)
+  // Two (four slices) or two and a half steps a wave at least.  4 bits, one / two / four waves: M = 333, K = 1056, N = 2047
+  // (nine steps) 8.9 / 7.6 / 8.0; M = 16, K = 1536, N = 4096 (six) 5.2 / 4.2 / 4.3; M = 40, K = 512, N = 2048 (four) 3.7 /
+  // 3.9 / 4.0; M = 100, K = 480, N = 2048 (four) 4.2 / 4.3 / 4.4; four slices, M = 2, K = N = 2048 (four) 3.9 / 3.4 / 3.2.  bf16:
+  // M = 64, K = 768, N = 1024 (six) 6.6 / 5.7 / 6.2; M = 8, K = 512, N = 2048 (two) 2.9 / 2.8 / 2.9.  The other way round by at most
+  // 0.4 us: bf16, M = 40, K = 512, N = 2048 4.6 / 4.2 / 4.5.
   while (p.waves > 1 && (p.slices == 4 ? 4 : 5) * p.waves * p.splits > 2 * steps) p.waves /= 2;
   return p;
 }
@@ -368,7 +372,7 @@ int launch_mx_stream(const MxStreamPlan& p, const MxGemmArgs& g, hipStream_t str
 // 12.5, M = 200 16.5 against 14.3; K = 5120, N = 5120: 19.6 against 26.0, 32.9 against 31.2), 65 on wide weights
 // (K = 5120, N = 17408: M = 64 32.3 against 33.2, M = 96 46.5 against 41.1; K = 1536, N = 9000: 9.5 against 9.6,
 // 14.1 against 11.1).  Where scale rows have to be padded first, by another launch, from 33 rows on and 2 10^9
-// products (4 bits, K = 2880, N = 201088: M = 4 65 against 110, M = 24 102 against 118, M = 33 132 against 121; K = 5152,
+// products (weights from HBM; 4 bits, K = 2880, N = 201088: M = 4 65 against 110, M = 24 102 against 118, M = 33 132 against 121; K = 5152,
 // N = 20000: M = 24 27.4 against 32.6, M = 33 32.8 against 33.1, M = 64 39.4 against 36.7; K = 2080, N = 8192: M = 64 9.2
 // against 12.2, M = 128 12.5 against 13.2, M = 333 26.1 against 17.2; K = 1056, N = 8192: M = 128 7.6 against 8.3,
 // M = 333 14.1 against 10.6; K = 17440, N = 5120: M = 24 24.4 against 31.8, M = 33 32.0 against 33.0).
