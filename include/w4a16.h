@@ -1,8 +1,9 @@
 /*
  * w4a16.h -- weight-only int4, group-128 quantized linear layers (W4A16) on
  * AMD CDNA4 (MI355X, gfx950): quantize + pack, decode GEMV, prefill GEMM and the
- * batched fake-quant loss of an AWQ scale-exponent / clip-shrink search; and linears in
- * MXFP4 (4-bit microscaling floats).
+ * batched fake-quant loss of an AWQ scale-exponent / clip-shrink search; linears in
+ * MXFP4 (4-bit microscaling floats); and the operators between a decoder's linears when it
+ * serves (norm with residual, rotary append to a paged cache, attention).
  *
  * Sources for what is computed (web pages, cited by title and section):
  *   [AWQ-W4 card]  model card "rebuttal_w4g128_awq_w2": details table rows
@@ -463,6 +464,122 @@ int mxfp4_a16_gemm(const uint16_t* X, int M, int K, int N, const uint32_t* qweig
                    uint16_t* Y, void* workspace, size_t* workspace_bytes, void* stream);
 int mxfp4_a4_gemm(const uint32_t* Xq, const uint8_t* xscales, int M, int K, int N, const uint32_t* qweight,
                   const uint8_t* scales, uint16_t* Y, void* workspace, size_t* workspace_bytes, void* stream);
+
+/*
+ * Serving operators: what a decoder runs between its quantized linears.  The block is
+ * that of w4_block_forward ([AWQ-W4 card] "Base model"; [q326 page] architecture notes);
+ * here sequences differ in length, keys and values live in a cache of pages, and the norm
+ * can hand int8 activations to w4a8_gemv.  Beside the conventions at the top of this file:
+ *   - head (the head size) is 64 or 128 (else W4_ERR_UNSUPPORTED); n_kv >= 1 divides n_q, and
+ *     query head i reads key/value head i / (n_q / n_kv).
+ *   - Packed arrays hold the tokens of all sequences one after another: [T][n][head] with
+ *     `stride` elements (a multiple of 8, at least n head) from one token to the next, so
+ *     that the parts of one fused projection can be passed as they are.  Outputs are
+ *     contiguous.  offsets [B+1] int32 device, ascending: sequence b holds the tokens
+ *     offsets[b] .. offsets[b+1]-1, possibly none.  Rows from offsets[B] on belong to no
+ *     sequence: they are not read, and the outputs' rows stay as they were.
+ *   - A cache: k, v [pages][n_kv][page_size][head] bf16, page_size 16, 32, 64, 128 or 256.
+ *     Token p of sequence b lies in slot p % page_size of page table[b][p / page_size]
+ *     (table [B][table_width] int32 device).
+ *   - What the host cannot see is held in range by the kernels, never followed: offsets
+ *     outside [0, T] count as the nearer end, a sequence whose offsets descend as empty,
+ *     lengths below 0 as 0; tokens whose page number lies outside [0, pages) or whose
+ *     position lies past the table are not written, and attention leaves such keys out.
+ *   - Keys and values that a query does not see (later tokens, other sequences, slots past
+ *     a sequence's length) may hold anything, NaN and infinities too.
+ *   - A call with no rows (T == 0 or B == 0) succeeds and enqueues nothing.  Outputs must
+ *     not overlap inputs or each other, unless said otherwise.
+ *
+ * w4_rmsnorm, w4a8_rmsnorm -- the residual's addition and the root-mean-square norm, as
+ *   bf16 or as w4a8_gemv's int8 activations:
+ *     h = bf16(X + residual)  (residual NULL: h = X),   r = 1 / sqrt(mean_k h^2 + eps),
+ *     w4_rmsnorm:    Y = bf16((h r) weight), in fp32;
+ *     w4a8_rmsnorm:  v = fp32(h weight), t = max_k |v| / 127 (1 where every v is 0),
+ *                    Xq = clamp(rint(v / t), -127, 127) (IEEE division, ties to even),
+ *                    sx = t r, xsum[m][g] = sum of Xq over the 128 channels of group g.
+ *   r multiplies a whole row, so it is left out of the codes and enters the scale: codes
+ *   and sums are bit-identical to this definition for every input, and Xq sx is the int8
+ *   form of the normed row.  A row with an infinite or NaN v gets codes 0 and sx NaN.
+ *   X, residual [T][H] bf16.  weight [H] bf16.  eps >= 0, finite (else W4_ERR_VALUE).
+ *   h [T][H] bf16 out, the new residual stream: required with a residual, and may be X or
+ *   residual itself; without one it must be NULL.  Y [T][H] bf16 out, may be X.
+ *   Xq [T][H] int8, sx [T] fp32, xsum [T][H/128] int32 out: w4a8_gemv reads any 16 rows of
+ *   them.  H a positive multiple of 8 (w4_rmsnorm) or 128 (w4a8_rmsnorm), at most 65,536
+ *   (else W4_ERR_SHAPE).
+ */
+int w4_rmsnorm(const uint16_t* X, const uint16_t* residual, int T, int H, const uint16_t* weight, float eps,
+               uint16_t* h, uint16_t* Y, void* stream);
+int w4a8_rmsnorm(const uint16_t* X, const uint16_t* residual, int T, int H, const uint16_t* weight, float eps,
+                 uint16_t* h, int8_t* Xq, float* sx, int32_t* xsum, void* stream);
+
+/* A paged cache: device arrays, host struct. */
+typedef struct w4_kv_cache {
+  uint16_t* k;      /* [pages][n_kv][page_size][head] bf16 */
+  uint16_t* v;
+  int pages;
+  int page_size;
+  int n_kv;
+  int head;
+} w4_kv_cache;
+
+/*
+ * w4_rope_table -- cs, sn [positions][head / 2] fp32 out: cosine and sine of
+ *   p base^(-2 j / head), in fp64, stored fp32.  base > 0, finite (else W4_ERR_VALUE).
+ */
+int w4_rope_table(int positions, int head, double base, float* cs, float* sn, void* stream);
+
+/*
+ * w4_kv_append -- the rotary embedding of new tokens' queries and keys, and their keys and
+ *   values into the cache.  Sequence b brings n_b = offsets[b+1] - offsets[b] tokens, after
+ *   which its cache holds lens[b]: its i-th new token sits at position lens[b] - n_b + i.
+ *   The pairs (j, j + head/2) turn as in w4_block_forward, by row `position` of cs, sn
+ *   [positions][head / 2]:  (x1 c - x2 s, x2 c + x1 s) in fp32, rounded to bf16.
+ *   Q [T][n_q][head], K and V [T][n_kv][head], each with its stride.
+ *   offsets NULL: one token per sequence (then T == B, else W4_ERR_SHAPE).
+ *   lens [B] int32 device.  Q_out [T][n_q][head] out; K_out [T][n_kv][head] out or NULL: the
+ *   turned keys beside the cache, as w4_prompt_attention reads them.  Q_out may be Q, and
+ *   K_out K, where the stride is n head.
+ *   A token whose position is negative or past cs, sn is left out: none of its rows is
+ *   written.  One that has no page (past the table, or a page number outside [0, pages))
+ *   gets its Q_out and K_out rows and no cache slot.  Two tokens of one call must not
+ *   share a slot.
+ */
+int w4_kv_append(const uint16_t* Q, long long q_stride, const uint16_t* K, long long k_stride, const uint16_t* V,
+                 long long v_stride, int T, int n_q, const int32_t* offsets, const int32_t* lens, int B,
+                 const int32_t* table, int table_width, const float* cs, const float* sn, int positions,
+                 const w4_kv_cache* cache, uint16_t* Q_out, uint16_t* K_out, void* stream);
+
+/*
+ * w4_prompt_attention -- causal attention of whole prompts: for token i of a sequence
+ *   O_i = sum_{j <= i} p_ij V_j / sum_{j <= i} p_ij,  p_ij = exp(scale Q_i . K_j - max_j),
+ *   over the sequence's own tokens j.  Q [T][n_q][head], K and V [T][n_kv][head], each with
+ *   its stride; O [T][n_q][head] bf16 out.  Products of bf16 values summed in fp32, maximum
+ *   and sums in fp32, p rounded to bf16 for the product with V, O rounded to nearest even.
+ *   scale > 0, finite (else W4_ERR_VALUE).
+ *   Size query and workspace as in w4a16_gemv; the size depends only on T, n_q, n_kv, head and B.
+ */
+int w4_prompt_attention(const uint16_t* Q, long long q_stride, const uint16_t* K, long long k_stride,
+                        const uint16_t* V, long long v_stride, int T, int n_q, int n_kv, int head,
+                        const int32_t* offsets, int B, float scale, uint16_t* O, void* workspace,
+                        size_t* workspace_bytes, void* stream);
+
+/*
+ * w4_decode_attention -- attention of one query per sequence over the cache:
+ *   O_b = softmax_p(scale Q_b . K_p) V over the tokens p < lens[b], arithmetic as in
+ *   w4_prompt_attention.  The first prefix_len tokens (a multiple of page_size, 0 for none)
+ *   are common to the batch: they are read once, from the pages in row 0 of the table; the
+ *   other rows' first prefix_len / page_size entries are not looked at.
+ *   Q [B][n_q][head] with its stride.  lens [B] int32 device; a sequence of length 0 gets zeros, one
+ *   shorter than the prefix sees its first lens[b] tokens.  max_len: no sequence is longer
+ *   (tokens from max_len on are left out); the work is laid out by it, lengths may change
+ *   between replays of a graph.  max_len and prefix_len at most table_width page_size.
+ *   O [B][n_q][head] bf16 out.
+ *   Size query and workspace as in w4a16_gemv; the size depends only on B, n_q, max_len,
+ *   prefix_len and the cache's page_size, n_kv and head (its pointers may be NULL then).
+ */
+int w4_decode_attention(const uint16_t* Q, long long q_stride, int B, int n_q, const w4_kv_cache* cache,
+                        const int32_t* lens, const int32_t* table, int table_width, int max_len, int prefix_len,
+                        float scale, uint16_t* O, void* workspace, size_t* workspace_bytes, void* stream);
 
 /*
  * Measurement helpers (not part of the method): the yardsticks the kernels

@@ -24,7 +24,8 @@ __all__ = [
     "w4a8_quantize_activations", "w4a8_gemv", "w4a8_gemv_launcher", "awq_clip_search", "block_forward",
     "block_forward_quantized", "awq_lookahead_loss", "awq_search_lookahead", "BLOCK_LINEARS", "probe_stream_read", "probe_empty",
     "MX_BLOCK", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_a16_gemm", "mxfp4_a4_gemm", "mxfp4_a16_gemm_launcher",
-    "mxfp4_a4_gemm_launcher",
+    "mxfp4_a4_gemm_launcher", "rmsnorm", "rmsnorm_launcher", "w4a8_rmsnorm", "w4a8_rmsnorm_launcher", "rope_table", "kv_append",
+    "kv_append_launcher", "prompt_attention", "prompt_attention_launcher", "decode_attention", "decode_attention_launcher",
 ]
 
 GROUP_SIZE = 128
@@ -44,7 +45,15 @@ class _Block(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in _BLOCK_FIELDS]
 
 
+class _KVCache(ctypes.Structure):
+    """struct w4_kv_cache: device pointers and sizes of a paged cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_kv", ctypes.c_int), ("head", ctypes.c_int)]
+
+
 _bp = ctypes.POINTER(_Block)
+_kv = ctypes.POINTER(_KVCache)
+_ll = ctypes.c_longlong
 _SIGNATURES = {
     "w4_status_string": ([_i], ctypes.c_char_p),
     "awq_quantize_pack": ([_vp, _i, _i, _vp, _f, _i, _i, _vp, _vp, _vp, _vp], _i),
@@ -70,6 +79,12 @@ _SIGNATURES = {
     "mxfp4_dequantize": ([_vp, _vp, _i, _i, _vp, _vp], _i),
     "mxfp4_a16_gemm": ([_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp], _i),
     "mxfp4_a4_gemm": ([_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp], _i),
+    "w4_rmsnorm": ([_vp, _vp, _i, _i, _vp, _f, _vp, _vp, _vp], _i),
+    "w4a8_rmsnorm": ([_vp, _vp, _i, _i, _vp, _f, _vp, _vp, _vp, _vp, _vp], _i),
+    "w4_rope_table": ([_i, _i, ctypes.c_double, _vp, _vp, _vp], _i),
+    "w4_kv_append": ([_vp, _ll, _vp, _ll, _vp, _ll, _i, _i, _vp, _vp, _i, _vp, _i, _vp, _vp, _i, _kv, _vp, _vp, _vp], _i),
+    "w4_prompt_attention": ([_vp, _ll, _vp, _ll, _vp, _ll, _i, _i, _i, _i, _vp, _i, _f, _vp, _vp, _sz, _vp], _i),
+    "w4_decode_attention": ([_vp, _ll, _i, _i, _kv, _vp, _vp, _i, _i, _i, _f, _vp, _vp, _sz, _vp], _i),
     "awq_search": ([_vp, _i, _i, _i, _vp, ctypes.POINTER(ctypes.c_double), _i,
                     ctypes.POINTER(ctypes.c_double), _i, _i, _i, ctypes.POINTER(ctypes.c_float),
                     ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int), _vp, _vp, _sz, _vp], _i),
@@ -715,6 +730,291 @@ def mxfp4_a16_gemm_launcher(X, qweight, scales, Y, workspace=None):
 def mxfp4_a4_gemm_launcher(Xq, xscales, qweight, scales, Y, workspace=None):
     """As gemv_launcher, for mxfp4_a4_gemm."""
     return _mx_gemm_launcher("mxfp4_a4_gemm", (Xq, xscales), qweight, scales, Y, workspace)[0]
+
+
+def _rows_of(t, name):
+    rows = t.shape[0]
+    if rows >> 31:                            # ctypes would keep the low 32 bits
+        raise ValueError(f"{name}: at most {2 ** 31 - 1} rows, got {rows}")
+    return rows
+
+
+def _bound(fn, args, index, tensors, ws=None, wsb=None):
+    """A zero-argument callable that enqueues the checked call on the current stream."""
+    def launch():
+        _mx_call(fn, args, index)
+
+    launch.tensors = tensors                  # kept alive while the launcher is
+    launch.workspace = ws
+    launch.workspace_size = wsb
+    return launch
+
+
+def _norm_args(X, weight, residual, H):
+    _need(X, torch.bfloat16, "X", 2)
+    rows, K = _rows_of(X, "X"), X.shape[1]
+    dev = X.device
+    _mx_need(weight, torch.bfloat16, "weight", (K,), dev)
+    if residual is None:
+        if H is not None:
+            raise ValueError("H is the sum X + residual: without a residual it must be None")
+        return rows, K, dev, None
+    _mx_need(residual, torch.bfloat16, "residual", (rows, K), dev)
+    if H is None:
+        H = torch.empty_like(X)
+    else:
+        _mx_need(H, torch.bfloat16, "H", (rows, K), dev)
+    return rows, K, dev, H
+
+
+def _rmsnorm(X, weight, residual, eps, Y, H):
+    lib = load_library()
+    rows, K, dev, H = _norm_args(X, weight, residual, H)
+    if Y is None:
+        Y = torch.empty_like(X)
+    else:
+        _mx_need(Y, torch.bfloat16, "Y", (rows, K), dev)
+    args = (_ptr(X), _ptr(residual), rows, K, _ptr(weight), float(eps), _ptr(H), _ptr(Y))
+    return _bound(lib.w4_rmsnorm, args, dev.index, (X, weight, residual, Y, H)), Y, H
+
+
+def rmsnorm(X, weight, residual=None, eps: float = 1e-6, Y=None, H=None):
+    """(Y, H): H = X + residual in bf16 (None without a residual), Y [T][K] bf16 its
+    root-mean-square norm times weight; see include/w4a16.h, w4_rmsnorm.  H may be X or residual."""
+    launch, Y, H = _rmsnorm(X, weight, residual, eps, Y, H)
+    launch()
+    return Y, H
+
+
+def rmsnorm_launcher(X, weight, residual, eps: float, Y, H=None):
+    """As gemv_launcher, for rmsnorm."""
+    return _rmsnorm(X, weight, residual, eps, Y, H)[0]
+
+
+def _w4a8_rmsnorm(X, weight, residual, eps, Xq, sx, xsum, H):
+    lib = load_library()
+    rows, K, dev, H = _norm_args(X, weight, residual, H)
+    if Xq is None:
+        Xq = torch.empty((rows, K), dtype=torch.int8, device=dev)
+    else:
+        _mx_need(Xq, torch.int8, "Xq", (rows, K), dev)
+    if sx is None:
+        sx = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        _mx_need(sx, torch.float32, "sx", (rows,), dev)
+    if xsum is None:
+        xsum = torch.empty((rows, K // GROUP_SIZE), dtype=torch.int32, device=dev)
+    else:
+        _mx_need(xsum, torch.int32, "xsum", (rows, K // GROUP_SIZE), dev)
+    args = (_ptr(X), _ptr(residual), rows, K, _ptr(weight), float(eps), _ptr(H), _ptr(Xq), _ptr(sx), _ptr(xsum))
+    return _bound(lib.w4a8_rmsnorm, args, dev.index, (X, weight, residual, Xq, sx, xsum, H)), (Xq, sx, xsum, H)
+
+
+def w4a8_rmsnorm(X, weight, residual=None, eps: float = 1e-6, Xq=None, sx=None, xsum=None, H=None):
+    """(Xq, sx, xsum, H): the normed rows of rmsnorm as w4a8_gemv's int8 activations, any
+    number of rows; H = X + residual in bf16 (None without a residual)."""
+    launch, out = _w4a8_rmsnorm(X, weight, residual, eps, Xq, sx, xsum, H)
+    launch()
+    return out
+
+
+def w4a8_rmsnorm_launcher(X, weight, residual, eps: float, Xq, sx, xsum, H=None):
+    """As gemv_launcher, for w4a8_rmsnorm."""
+    return _w4a8_rmsnorm(X, weight, residual, eps, Xq, sx, xsum, H)[0]
+
+
+def rope_table(positions: int, head: int = 128, base: float = 1e6, device="cuda"):
+    """(cs, sn) fp32 [positions][head / 2]: the rotary angles' cosines and sines for kv_append."""
+    lib = load_library()
+    if positions < 0 or positions >> 31:
+        raise ValueError(f"positions must be in [0, {2 ** 31 - 1}], got {positions}")
+    cs = torch.empty((positions, head // 2), dtype=torch.float32, device=device)
+    sn = torch.empty_like(cs)
+    if not cs.is_cuda:
+        raise ValueError("device must be a GPU")
+    _mx_call(lib.w4_rope_table, (positions, head, float(base), _ptr(cs), _ptr(sn)), cs.device.index)
+    return cs, sn
+
+
+def _heads(t, name, rows, head, device):
+    """(heads, stride) of [rows][heads][head] bf16 whose tokens lie `stride` elements apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != head:
+        raise ValueError(f"{name} must have shape ({rows}, heads, {head}), got {tuple(t.shape)}")
+    n = t.shape[1]
+    if n >> 31:
+        raise ValueError(f"{name}: too many heads, {n}")
+    if (n > 1 and t.stride(1) != head) or (head > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return n, t.stride(0) if rows > 1 else max(n * head, 8)
+
+
+def _cache_struct(k_cache, v_cache):
+    _need(k_cache, torch.bfloat16, "k_cache", 4)
+    pages, n_kv, page_size, head = k_cache.shape
+    _mx_need(v_cache, torch.bfloat16, "v_cache", tuple(k_cache.shape), k_cache.device)
+    if (pages | n_kv | page_size | head) >> 31:
+        raise ValueError("k_cache: sizes must fit an int")
+    return _KVCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size, n_kv, head)
+
+
+def _table_width(table, B, device):
+    _need(table, torch.int32, "table", 2)
+    width = table.shape[1]
+    _mx_need(table, torch.int32, "table", (B, width), device)
+    if width >> 31:
+        raise ValueError("table: too many pages in a row")
+    return width
+
+
+def _kv_append(Q, K, V, cs, sn, k_cache, v_cache, lens, table, offsets, Q_out, K_out):
+    lib = load_library()
+    cache = _cache_struct(k_cache, v_cache)
+    dev, head = k_cache.device, cache.head
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
+        raise ValueError("Q must be a tensor [T][n_q][head]")
+    T = _rows_of(Q, "Q")
+    n_q, q_stride = _heads(Q, "Q", T, head, dev)
+    n_kv, k_stride = _heads(K, "K", T, head, dev)
+    n_v, v_stride = _heads(V, "V", T, head, dev)
+    if n_kv != cache.n_kv or n_v != cache.n_kv:
+        raise ValueError(f"K and V must have the cache's {cache.n_kv} heads, got {n_kv} and {n_v}")
+    _need(lens, torch.int32, "lens", 1)
+    B = _rows_of(lens, "lens")
+    _mx_need(lens, torch.int32, "lens", (B,), dev)
+    if offsets is not None:
+        _mx_need(offsets, torch.int32, "offsets", (B + 1,), dev)
+    width = _table_width(table, B, dev)
+    _need(cs, torch.float32, "cs", 2)
+    positions = _rows_of(cs, "cs")
+    _mx_need(cs, torch.float32, "cs", (positions, head // 2), dev)
+    _mx_need(sn, torch.float32, "sn", (positions, head // 2), dev)
+    if Q_out is None:
+        Q_out = torch.empty((T, n_q, head), dtype=torch.bfloat16, device=dev)
+    else:
+        _mx_need(Q_out, torch.bfloat16, "Q_out", (T, n_q, head), dev)
+    if K_out is not None:
+        _mx_need(K_out, torch.bfloat16, "K_out", (T, n_kv, head), dev)
+    args = (_ptr(Q), q_stride, _ptr(K), k_stride, _ptr(V), v_stride, T, n_q, _ptr(offsets), _ptr(lens), B, _ptr(table), width,
+            _ptr(cs), _ptr(sn), positions, ctypes.byref(cache), _ptr(Q_out), _ptr(K_out))
+    keep = (Q, K, V, cs, sn, k_cache, v_cache, lens, table, offsets, Q_out, K_out, cache)
+    return _bound(lib.w4_kv_append, args, dev.index, keep), Q_out
+
+
+def kv_append(Q, K, V, cs, sn, k_cache, v_cache, lens, table, offsets=None, Q_out=None, K_out=None):
+    """Turn the new tokens' queries and keys and put keys and values into the paged cache.
+
+    Q [T][n_q][head], K and V [T][n_kv][head] bf16 (views of one fused projection will do);
+    cs, sn from rope_table; k_cache, v_cache [pages][n_kv][page_size][head]; lens [B] int32
+    lengths after the append; table [B][pages of a sequence] int32; offsets [B + 1] int32, or
+    None for one token a sequence.  Returns (Q_out, K_out); K_out, the turned keys in packed
+    form, is written only if given.  See include/w4a16.h, w4_kv_append."""
+    launch, Q_out = _kv_append(Q, K, V, cs, sn, k_cache, v_cache, lens, table, offsets, Q_out, K_out)
+    launch()
+    return Q_out, K_out
+
+
+def kv_append_launcher(Q, K, V, cs, sn, k_cache, v_cache, lens, table, offsets, Q_out, K_out=None):
+    """As gemv_launcher, for kv_append."""
+    return _kv_append(Q, K, V, cs, sn, k_cache, v_cache, lens, table, offsets, Q_out, K_out)[0]
+
+
+def _prompt_attention(Q, K, V, offsets, scale, O, workspace):
+    lib = load_library()
+    _need(offsets, torch.int32, "offsets", 1)
+    dev = offsets.device
+    B = _rows_of(offsets, "offsets") - 1
+    if B < 0:
+        raise ValueError("offsets must have a place per sequence and one more")
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
+        raise ValueError("Q must be a tensor [T][n_q][head]")
+    T, head = _rows_of(Q, "Q"), Q.shape[2]
+    n_q, q_stride = _heads(Q, "Q", T, head, dev)
+    n_kv, k_stride = _heads(K, "K", T, head, dev)
+    if _heads(V, "V", T, head, dev)[0] != n_kv:
+        raise ValueError("K and V must have the same heads")
+    v_stride = _heads(V, "V", T, head, dev)[1]
+    if O is None:
+        O = torch.empty((T, n_q, head), dtype=torch.bfloat16, device=dev)
+    else:
+        _mx_need(O, torch.bfloat16, "O", (T, n_q, head), dev)
+    if workspace is not None:
+        _mx_need(workspace, torch.uint8, "workspace", (workspace.numel(),), dev)
+
+    def q(sz):
+        return lib.w4_prompt_attention(None, 0, None, 0, None, 0, T, n_q, n_kv, head, None, B, 0.0, None, None, sz, None)
+
+    ws, wsb = _workspace(q, dev, workspace)
+    args = (_ptr(Q), q_stride, _ptr(K), k_stride, _ptr(V), v_stride, T, n_q, n_kv, head, _ptr(offsets), B,
+            head ** -0.5 if scale is None else float(scale), _ptr(O), _ptr(ws), None if wsb is None else ctypes.byref(wsb))
+    return _bound(lib.w4_prompt_attention, args, dev.index, (Q, K, V, offsets, O, ws), ws, wsb), O
+
+
+def prompt_attention(Q, K, V, offsets, scale=None, O=None, workspace=None):
+    """Causal attention of packed prompts: O [T][n_q][head] bf16 from Q [T][n_q][head], K and V
+    [T][n_kv][head] bf16 (views of one fused projection will do) and offsets [B + 1] int32;
+    scale 1 / sqrt(head) unless given.  Rows past offsets[B] are left as they were.  See
+    include/w4a16.h, w4_prompt_attention."""
+    launch, O = _prompt_attention(Q, K, V, offsets, scale, O, workspace)
+    launch()
+    return O
+
+
+def prompt_attention_launcher(Q, K, V, offsets, scale=None, O=None, workspace=None):
+    """As gemv_launcher, for prompt_attention."""
+    return _prompt_attention(Q, K, V, offsets, scale, O, workspace)[0]
+
+
+def _decode_attention(Q, k_cache, v_cache, lens, table, max_len, prefix_len, scale, O, workspace):
+    lib = load_library()
+    cache = _cache_struct(k_cache, v_cache)
+    dev, head = k_cache.device, cache.head
+    _need(lens, torch.int32, "lens", 1)
+    B = _rows_of(lens, "lens")
+    _mx_need(lens, torch.int32, "lens", (B,), dev)
+    n_q, q_stride = _heads(Q, "Q", B, head, dev)
+    width = _table_width(table, B, dev)
+    if max_len is None:
+        max_len = min(width * cache.page_size, 2 ** 31 - 1)
+    if not 0 <= max_len < 2 ** 31 or not 0 <= prefix_len < 2 ** 31:
+        raise ValueError("max_len and prefix_len must be whole numbers of tokens below 2^31")
+    if O is None:
+        O = torch.empty((B, n_q, head), dtype=torch.bfloat16, device=dev)
+    else:
+        _mx_need(O, torch.bfloat16, "O", (B, n_q, head), dev)
+    if workspace is not None:
+        _mx_need(workspace, torch.uint8, "workspace", (workspace.numel(),), dev)
+    ref = ctypes.byref(cache)
+
+    def q(sz):
+        return lib.w4_decode_attention(None, 0, B, n_q, ref, None, None, 0, max_len, prefix_len, 0.0, None, None, sz, None)
+
+    ws, wsb = _workspace(q, dev, workspace)
+    args = (_ptr(Q), q_stride, B, n_q, ref, _ptr(lens), _ptr(table), width, max_len, prefix_len,
+            head ** -0.5 if scale is None else float(scale), _ptr(O), _ptr(ws), None if wsb is None else ctypes.byref(wsb))
+    return _bound(lib.w4_decode_attention, args, dev.index, (Q, k_cache, v_cache, lens, table, O, ws, cache), ws, wsb), O
+
+
+def decode_attention(Q, k_cache, v_cache, lens, table, max_len=None, prefix_len: int = 0, scale=None, O=None, workspace=None):
+    """Attention of one query per sequence over the paged cache: O [B][n_q][head] bf16 from Q
+    [B][n_q][head], the cache, lens [B] int32 and table [B][pages of a sequence] int32.  max_len
+    bounds every length (default: what the table can hold) and lays out the work; the first
+    prefix_len tokens, whole pages, are common to the batch and read once, from row 0's pages.
+    scale 1 / sqrt(head) unless given.  See include/w4a16.h, w4_decode_attention."""
+    launch, O = _decode_attention(Q, k_cache, v_cache, lens, table, max_len, prefix_len, scale, O, workspace)
+    launch()
+    return O
+
+
+def decode_attention_launcher(Q, k_cache, v_cache, lens, table, max_len=None, prefix_len: int = 0, scale=None, O=None,
+                              workspace=None):
+    """As gemv_launcher, for decode_attention."""
+    return _decode_attention(Q, k_cache, v_cache, lens, table, max_len, prefix_len, scale, O, workspace)[0]
 
 
 def probe_stream_read(buf, unroll: int = 4, nontemporal: bool = False, blocks: int = 0, sink=None):

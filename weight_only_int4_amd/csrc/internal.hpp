@@ -178,6 +178,77 @@ struct MxPlan {
 MxPlan plan_mxfp4_gemm(int act_bits, int M, int K, int N);
 int launch_mxfp4_gemm(const MxPlan& p, const MxGemmArgs& g, hipStream_t stream);
 
+// ---------------------------------------------------------------- serving operators
+// The *_fits functions say whether a launch stays within a grid's limits.
+struct NormArgs {
+  const uint16_t *X, *residual;   // [T][H]; residual may be NULL
+  int T, H;
+  const uint16_t* weight;         // [H]
+  float eps;
+  uint16_t *h, *Y;                // [T][H]; Y, or the three below
+  int8_t* Xq;                     // [T][H]
+  float* sx;                      // [T]
+  int32_t* xsum;                  // [T][H/128]
+};
+bool norm_fits(int T);
+int launch_norm(const NormArgs& a, hipStream_t stream);
+
+bool rope_table_fits(int positions, int head);
+int launch_rope_table(int positions, int head, double base, float* cs, float* sn, hipStream_t stream);
+
+struct AppendArgs {
+  const uint16_t* Q;
+  long long q_stride;
+  const uint16_t* K;
+  long long k_stride;
+  const uint16_t* V;
+  long long v_stride;
+  int T, n_q;
+  const int32_t *offsets, *lens;  // [B+1] or NULL, [B]
+  int B;
+  const int32_t* table;           // [B][table_width]
+  int table_width;
+  const float *cs, *sn;           // [positions][head/2]
+  int positions;
+  w4_kv_cache cache;
+  uint16_t *Q_out, *K_out;
+};
+bool append_fits(int T);
+int launch_kv_append(const AppendArgs& g, hipStream_t stream);
+
+struct PromptArgs {
+  const uint16_t* Q;
+  long long q_stride;
+  const uint16_t* K;
+  long long k_stride;
+  const uint16_t* V;
+  long long v_stride;
+  int T, n_q, n_kv, head;
+  const int32_t* offsets;         // [B+1]
+  int B;
+  float scale;
+  uint16_t* O;
+  void* workspace;
+};
+bool prompt_fits(int T, int n_q);
+size_t prompt_workspace_bytes(int T, int n_q, int n_kv, int head, int B);
+int launch_prompt_attention(const PromptArgs& g, hipStream_t stream);
+
+struct DecodeArgs {
+  const uint16_t* Q;
+  long long q_stride;
+  int B, n_q;
+  w4_kv_cache cache;
+  const int32_t *lens, *table;    // [B], [B][table_width]
+  int table_width, max_len, prefix_len;
+  float scale;
+  uint16_t* O;
+  void* workspace;
+};
+bool decode_fits(int B, int n_q);
+size_t decode_workspace_bytes(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len);
+int launch_decode_attention(const DecodeArgs& g, hipStream_t stream);
+
 // m_k = mean_t |X[t][k]| in fp64, fixed summation order.
 // m must hold (1 + ceil(T / 64)) * K doubles: m[0..K) is the result, the rest
 // per-chunk partial sums.

@@ -1,0 +1,160 @@
+// The residual's addition and the root-mean-square norm, out in bf16 (w4_rmsnorm) or as the
+// int8 activations of the W4A8 linears (w4a8_rmsnorm).
+//   h = bf16(x + residual), r = 1 / sqrt(mean h^2 + eps);  y = bf16((h r) w);
+//   v = fp32(h w), t = max |v| / 127, codes = clamp(rint(v / t)), sx = t r.
+// r > 0 is common to a row's values, so rint(y / (max |y| / 127)) does not depend on it: taking
+// the codes from v keeps them exact (v is, both factors having 8-bit significands), while r,
+// whose last bit depends on the order of a sum, enters the scale alone.
+#include "serve.hpp"
+
+#pragma clang fp contract(off)
+
+namespace w4 {
+
+namespace {
+
+constexpr int kNormThreads = 256;
+
+__device__ __forceinline__ int row16_sum(int v) {
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);
+  return v;
+}
+
+// One workgroup per row; thread i holds the 8-channel chunks i, i + 256, ... of h, so the row is
+// read once.
+template <int CH, bool INT8>
+__global__ __launch_bounds__(kNormThreads) void norm_kernel(const uint16_t* X, const uint16_t* R, int H,
+                                                            const uint16_t* __restrict__ w, float eps, uint16_t* hout,
+                                                            uint16_t* Y, int8_t* Xq, float* sx, int32_t* xsum) {
+  __shared__ float red[2][kNormThreads / kWave];
+  const size_t row = blockIdx.x;
+  const int tid = threadIdx.x, chunks = H >> 3;
+  uint4 hv[CH];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = tid + i * kNormThreads;
+    hv[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (c >= chunks) continue;
+    hv[i] = *reinterpret_cast<const uint4*>(X + row * H + 8 * c);
+    uint32_t* d = reinterpret_cast<uint32_t*>(&hv[i]);
+    if (R) {
+      const uint4 rv = *reinterpret_cast<const uint4*>(R + row * H + 8 * c);
+      const uint32_t e[4] = {rv.x, rv.y, rv.z, rv.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const bf16x2 s = {(__bf16)(__uint_as_float(d[q] << 16) + __uint_as_float(e[q] << 16)),
+                          (__bf16)(__uint_as_float(d[q] & 0xFFFF0000u) + __uint_as_float(e[q] & 0xFFFF0000u))};
+        d[q] = __builtin_bit_cast(uint32_t, s);
+      }
+      *reinterpret_cast<uint4*>(hout + row * H + 8 * c) = hv[i];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float a = __uint_as_float(d[q] << 16), b = __uint_as_float(d[q] & 0xFFFF0000u);
+      ss = ss + a * a;
+      ss = ss + b * b;
+    }
+  }
+  ss = wave_sum(ss);
+  if ((tid & 63) == 0) red[0][tid >> 6] = ss;
+  __syncthreads();
+  ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kNormThreads / kWave; ++i) ss = ss + red[0][i];
+  const float r = 1.0f / sqrtf(ss / (float)H + eps);
+  if constexpr (!INT8) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = tid + i * kNormThreads;
+      if (c >= chunks) continue;
+      const uint4 wv = *reinterpret_cast<const uint4*>(w + 8 * c);
+      const uint32_t d[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w}, e[4] = {wv.x, wv.y, wv.z, wv.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const bf16x2 y = {(__bf16)((__uint_as_float(d[q] << 16) * r) * __uint_as_float(e[q] << 16)),
+                          (__bf16)((__uint_as_float(d[q] & 0xFFFF0000u) * r) * __uint_as_float(e[q] & 0xFFFF0000u))};
+        o[q] = __builtin_bit_cast(uint32_t, y);
+      }
+      *reinterpret_cast<uint4*>(Y + row * H + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  } else {
+    // max |v| as a maximum of bit patterns: NaN counts as the largest
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = tid + i * kNormThreads;
+      if (c >= chunks) continue;
+      const uint4 wv = *reinterpret_cast<const uint4*>(w + 8 * c);
+      const uint32_t d[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w}, e[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        top = max(top, __float_as_uint(__uint_as_float(d[q] << 16) * __uint_as_float(e[q] << 16)) & 0x7FFFFFFFu);
+        top = max(top, __float_as_uint(__uint_as_float(d[q] & 0xFFFF0000u) * __uint_as_float(e[q] & 0xFFFF0000u)) &
+                           0x7FFFFFFFu);
+      }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, kWave));
+    if ((tid & 63) == 0) red[1][tid >> 6] = __uint_as_float(top);
+    __syncthreads();
+    top = 0u;
+#pragma unroll
+    for (int i = 0; i < kNormThreads / kWave; ++i) top = max(top, __float_as_uint(red[1][i]));
+    const bool finite = top < 0x7F800000u;
+    const float t = top ? __uint_as_float(top) / 127.0f : 1.0f;
+    if (tid == 0) sx[row] = finite ? t * r : __uint_as_float(0x7FC00000u);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = tid + i * kNormThreads;
+      int part = 0;
+      if (c < chunks) {
+        const uint4 wv = *reinterpret_cast<const uint4*>(w + 8 * c);
+        const uint32_t d[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w}, e[4] = {wv.x, wv.y, wv.z, wv.w};
+        uint32_t packed[2] = {0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t a = (j & 1) ? (d[j >> 1] & 0xFFFF0000u) : (d[j >> 1] << 16);
+          const uint32_t b = (j & 1) ? (e[j >> 1] & 0xFFFF0000u) : (e[j >> 1] << 16);
+          const float q = __builtin_rintf((__uint_as_float(a) * __uint_as_float(b)) / t);
+          const int code = finite ? (int)fminf(fmaxf(q, -127.0f), 127.0f) : 0;
+          part += code;
+          packed[j >> 2] |= ((uint32_t)code & 0xFFu) << (8 * (j & 3));
+        }
+        *reinterpret_cast<uint2*>(Xq + row * H + 8 * c) = make_uint2(packed[0], packed[1]);
+      }
+      part = row16_sum(part);                       // 16 lanes x 8 channels: one group
+      if ((tid & 15) == 0 && c < chunks) xsum[row * (H >> 7) + (c >> 4)] = part;
+    }
+  }
+}
+
+template <int CH>
+void launch(const NormArgs& a, hipStream_t st) {
+  if (a.Xq)
+    hipLaunchKernelGGL((norm_kernel<CH, true>), dim3(a.T), dim3(kNormThreads), 0, st, a.X, a.residual, a.H, a.weight,
+                       a.eps, a.h, a.Y, a.Xq, a.sx, a.xsum);
+  else
+    hipLaunchKernelGGL((norm_kernel<CH, false>), dim3(a.T), dim3(kNormThreads), 0, st, a.X, a.residual, a.H, a.weight,
+                       a.eps, a.h, a.Y, a.Xq, a.sx, a.xsum);
+}
+
+}  // namespace
+
+bool norm_fits(int T) { return (long long)T * kNormThreads <= kGridThreads; }
+
+int launch_norm(const NormArgs& a, hipStream_t st) {
+  const int per = (a.H / 8 + kNormThreads - 1) / kNormThreads;
+  if (per <= 1) launch<1>(a, st);
+  else if (per <= 2) launch<2>(a, st);
+  else if (per <= 4) launch<4>(a, st);
+  else if (per <= 8) launch<8>(a, st);
+  else if (per <= 16) launch<16>(a, st);
+  else launch<32>(a, st);
+  W4_CHECK_LAUNCH();
+  return W4_OK;
+}
+
+}  // namespace w4

@@ -1,0 +1,36 @@
+// Shared parts of the serving operators: norm, rotary append to the paged cache, prompt and
+// single-token attention.  See include/w4a16.h for what each computes.
+#pragma once
+
+#include "internal.hpp"
+
+namespace w4 {
+
+// Most threads along one dimension of a grid (its size in work items is a 32-bit field).
+constexpr long long kGridThreads = 0xFFFFFFFFLL;
+
+// Token offset i of a packed batch, held inside [0, T] whatever the array says.
+__device__ __forceinline__ int token_offset(const int32_t* offsets, int i, int T) {
+  return min(max(offsets[i], 0), T);
+}
+
+// The sequence that token t of a packed batch belongs to, or -1: the last b with
+// offsets[b] <= t, if t < offsets[b + 1].  All 64 lanes of the wave take part, with the same t:
+// each step asks 64 places at once, so up to 4,096 sequences take two round trips.
+__device__ __forceinline__ int find_sequence(const int32_t* offsets, int B, int t) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 63) / 64;
+    const int i = lane * step;
+    const bool before = i < n && offsets[lo + i] <= t;
+    const int c = __popcll(__ballot(before));
+    if (c == 0) return -1;                         // (of ascending offsets only the first can lie behind t)
+    const int skip = min((c - 1) * step, n - 1);
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return offsets[lo] <= t && t < offsets[lo + 1] ? lo : -1;
+}
+
+}  // namespace w4
