@@ -473,7 +473,7 @@ int mxfp4_a4_gemm(const uint32_t* Xq, const uint8_t* xscales, int M, int K, int 
  *   - head (the head size) is 64 or 128 (else W4_ERR_UNSUPPORTED); n_kv >= 1 divides n_q, and
  *     query head i reads key/value head i / (n_q / n_kv).
  *   - Packed arrays hold the tokens of all sequences one after another: [T][n][head] with
- *     `stride` elements (a multiple of 8, at least n head) from one token to the next, so
+ *     `stride` elements (a multiple of 8, n head to 2^24) from one token to the next, so
  *     that the parts of one fused projection can be passed as they are.  Outputs are
  *     contiguous.  offsets [B+1] int32 device, ascending: sequence b holds the tokens
  *     offsets[b] .. offsets[b+1]-1, possibly none.  Rows from offsets[B] on belong to no

@@ -284,8 +284,8 @@ def test_append_past_32_bit_offsets():
     kc = torch.empty(pages, n_kv, page, head, dtype=BF, device="cuda")
     vc = torch.empty_like(kc)
     kc[-3:], vc[-3:] = 3, 3
-    base = torch.empty(130 << 25, dtype=BF, device="cuda")
-    far = lambda n, at: base.as_strided((130, n, head), (1 << 25, head, 1), at * head)  # noqa: E731
+    base = torch.empty(130 << 24, dtype=BF, device="cuda")
+    far = lambda n, at: base.as_strided((130, n, head), (1 << 24, head, 1), at * head)  # noqa: E731
     q, k, v = normal(rng, 130, 8, head), normal(rng, 130, 8, head), normal(rng, 130, 8, head)
     gq, gk, gv = far(8, 0), far(8, 8), far(8, 16)
     gq.copy_(gpu(q)), gk.copy_(gpu(k)), gv.copy_(gpu(v))

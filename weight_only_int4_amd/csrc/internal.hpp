@@ -230,7 +230,7 @@ struct PromptArgs {
   uint16_t* O;
   void* workspace;
 };
-bool prompt_fits(int T, int n_q);
+bool prompt_fits(int T, int n_q, int n_kv, int B);
 size_t prompt_workspace_bytes(int T, int n_q, int n_kv, int head, int B);
 int launch_prompt_attention(const PromptArgs& g, hipStream_t stream);
 

@@ -9,6 +9,10 @@ namespace w4 {
 // Most threads along one dimension of a grid (its size in work items is a 32-bit field).
 constexpr long long kGridThreads = 0xFFFFFFFFLL;
 
+// Most elements from one token to the next: 64 tokens stay below 2^32 bytes, the range of a
+// copy's 32-bit offset.
+constexpr long long kMaxStride = 1LL << 24;
+
 // Token offset i of a packed batch, held inside [0, T] whatever the array says.
 __device__ __forceinline__ int token_offset(const int32_t* offsets, int i, int T) {
   return min(max(offsets[i], 0), T);

@@ -28,7 +28,7 @@ int check_heads(int n_q, int n_kv, int head) {
 
 // one token of n heads every `stride` elements
 int check_stride(long long stride, int n, int head) {
-  return stride % 8 || stride < (long long)n * head || stride > (1LL << 40) ? W4_ERR_SHAPE : W4_OK;
+  return stride % 8 || stride < (long long)n * head || stride > kMaxStride ? W4_ERR_SHAPE : W4_OK;
 }
 
 int check_cache(const w4_kv_cache& c, int n_q) {
@@ -103,7 +103,7 @@ int w4_prompt_attention(const uint16_t* Q, long long q_stride, const uint16_t* K
                         long long v_stride, int T, int n_q, int n_kv, int head, const int32_t* offsets, int B,
                         float scale, uint16_t* O, void* workspace, size_t* workspace_bytes, void* stream) {
   if (int st = check_heads(n_q, n_kv, head)) return st;
-  if (T < 0 || B < 0 || !prompt_fits(T, n_q)) return W4_ERR_SHAPE;
+  if (T < 0 || B < 0 || !prompt_fits(T, n_q, n_kv, B)) return W4_ERR_SHAPE;
   const size_t need = prompt_workspace_bytes(T, n_q, n_kv, head, B);
   if (!workspace && workspace_bytes) {
     *workspace_bytes = need;
