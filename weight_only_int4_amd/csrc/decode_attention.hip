@@ -1,5 +1,12 @@
-// Attention of single tokens over the paged cache: the plain kernel, one wave per (query, head).
+// Attention of single tokens over the paged cache, a prefix common to the batch read once.
+//
+// The keys are split: the prefix into chunks that all sequences' queries of a key/value head see together
+// (as many rows as the batch has sequences times the group), each sequence's own tokens into chunks of their
+// own.  Every chunk gives, per row, the largest score m, the sum l of p = exp(scale (s - m)) and sum p V in
+// fp32; a second kernel joins a row's chunks: O = sum_c w_c O_c / sum_c w_c l_c, w_c = exp(scale (m_c - max m)).
+// Chunk sizes follow from what the host knows, so a captured graph serves any lengths.
 #include "attend.hpp"
+#include "gemm_core.hpp"
 
 #pragma clang fp contract(off)
 
@@ -7,38 +14,395 @@ namespace w4 {
 
 namespace {
 
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kSlack = 8.0f;                // see the prompt kernel: the reference lags the maximum by at most 2^8
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
+
+struct DecodePlan {
+  int group, wide;            // queries of a key/value head; prefix rows go 128 to a workgroup (else 16)
+  int p_chunk, p_splits, p_tiles;    // prefix: keys of a chunk, chunks, row tiles
+  int o_chunk, o_splits, o_tiles;    // own tokens
+  int splits;
+  size_t rows, stats_bytes, bytes;   // rows of the batch; workspace: [splits][rows][2], then [splits][rows][head]
+};
+
+// Everything a workgroup needs of a row: where its query lies and how far it sees.
+struct Row {
+  int b, hq, limit;
+};
+
+struct Kernel {
+  DecodeArgs g;
+  DecodePlan p;
+  float* stats;               // NULL: one chunk in all, the output is written at once
+  float* part;
+};
+
+// Page numbers of 64 table entries, one per lane; a lane index past them moves the window.
+struct Pages {
+  const int32_t* row;
+  int width, pages, base, held;
+  __device__ __forceinline__ void load(int entry) {
+    const int e = entry + (threadIdx.x & 63);
+    base = entry;
+    held = e < width ? row[e] : -1;
+  }
+  // page of a (wave-uniform) entry, -1 if there is none
+  __device__ __forceinline__ int operator()(int entry) {
+    if (entry - base >= 64) load(entry);
+    const int page = __builtin_amdgcn_readlane(held, entry - base);
+    return (unsigned)page < (unsigned)pages ? page : -1;
+  }
+};
+
+// One chunk of keys [key0, end) for up to 16 rows; four waves take its tiles of 32 keys in turn,
+// each by itself: K straight into registers as the operand of S^T = K Q^T
+// (v_mfma_f32_16x16x32_bf16), V through LDS, from where the transposing read gives the operand of
+// O^T += V^T P^T; the next tile's loads run meanwhile.
 template <int HEAD>
-__global__ __launch_bounds__(256) void decode_kernel(DecodeArgs g) {
-  const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (item >= (long long)g.B * g.n_q) return;
-  const int b = (int)(item / g.n_q), h = (int)(item - (long long)b * g.n_q);
-  const int n = min(max(g.lens[b], 0), g.max_len);
-  const int kvh = h / (g.n_q / g.cache.n_kv);
+__device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh, const int32_t* table_row, int key0,
+                             int end, int split, unsigned char* smem) {
+  constexpr int kSteps = HEAD / 32, kDb = HEAD / 16, kRowB = 2 * HEAD, kChunks = HEAD / 8;
+  constexpr int kRowsPer = 64 / kChunks, kLoads = 32 / kRowsPer;      // V rows of one load, loads of a tile
+  const DecodeArgs& g = k.g;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, qd = lane >> 4;
   const int page_size = g.cache.page_size, shift = __builtin_ctz(page_size);
-  attend<HEAD>(g.Q + (size_t)b * g.q_stride + (size_t)h * HEAD, n, g.scale,
+  const size_t page_elems = (size_t)g.cache.n_kv * page_size * HEAD;
+  const size_t head_off = (size_t)kvh * page_size * HEAD;
+  unsigned char* vlds = smem + wave * 32 * kRowB;
+
+  bf16x8 qf[kSteps];
+  {
+    const uint16_t* qp = g.Q + (size_t)row.b * g.q_stride + (size_t)row.hq * HEAD + 8 * qd;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) qf[st] = *reinterpret_cast<const bf16x8*>(qp + 32 * st);
+  }
+  const float c = g.scale * kLog2e, slack = kSlack / c;
+  f32x4_t acc[kDb];
+#pragma unroll
+  for (int db = 0; db < kDb; ++db) acc[db] = f32x4_t{};
+  float mref = -INFINITY, lsum = 0.0f;
+
+  // V rows in LDS: piece c of row r at c ^ swap(r): a transposing read takes 8 rows, 32 bytes each
+  auto swap = [](int r) { return HEAD == 128 ? (r & 7) * 2 : ((r >> 1) & 3) * 2; };
+  const int vrow = lane / kChunks, vpiece = lane % kChunks;
+  uint32_t vwrite[kLoads];
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int r = vrow + j * kRowsPer;
+    vwrite[j] = r * kRowB + 16 * (vpiece ^ swap(r));
+  }
+  const int tr = 4 * qd + (l16 >> 2);
+  const uint32_t vread = tr * kRowB + 16 * (((l16 & 3) >> 1) ^ swap(tr)) + 8 * (l16 & 1);
+
+  bf16x8 kf[2][kSteps];
+  uint4 vf[kLoads];
+  int missing = 0, missing_next = 0;          // bits: the tile's 16-key halves that have no page
+  Pages pages{table_row, g.table_width, g.cache.pages, 0, 0};
+  auto load_tile = [&](int kb) {              // kb < end; keys past the end repeat the last one
+    missing_next = 0;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      const int k0 = min(kb + 16 * a, (end - 1) & ~15), last = end - 1 - k0;      // last: 0 .. (15 and more)
+      const int page = pages(k0 >> shift);
+      if (page < 0) missing_next |= 1 << a;
+      const size_t at = (size_t)max(page, 0) * page_elems + head_off + (size_t)(k0 & (page_size - 1)) * HEAD;
+      const uint16_t* kp = g.cache.k + at;
+      const uint16_t* vp = g.cache.v + at;
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st)
+        kf[a][st] = *reinterpret_cast<const bf16x8*>(kp + (uint32_t)(min(l16, last) * HEAD + 32 * st + 8 * qd));
+#pragma unroll
+      for (int j = 0; j < kLoads / 2; ++j)
+        vf[a * (kLoads / 2) + j] =
+            *reinterpret_cast<const uint4*>(vp + (uint32_t)(min(vrow + j * kRowsPer, last) * HEAD + 8 * vpiece));
+    }
+  };
+  const int first = key0 + wave * 32;
+  const bool work = first < end && g.cache.pages > 0;
+  if (work) {
+    pages.load(first >> shift);
+    load_tile(first);
+    for (int kb = first; kb < end; kb += 128) {
+      missing = missing_next;
+      f32x4_t s[2];
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        s[a] = f32x4_t{};
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)
+          s[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[a][st], qf[st], s[a], 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) *reinterpret_cast<uint4*>(vlds + vwrite[j]) = vf[j];
+      if (kb + 128 < end) load_tile(kb + 128);
+      const int last = min(end, row.limit) - kb - 4 * qd;       // keys from here on are not this row's
+      if (__ballot(last < 32 - 4 * qd) || missing) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (16 * a + r >= last || (missing >> a & 1)) s[a][r] = -INFINITY;
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int r = 1; r < 8; ++r) top = fmaxf(top, s[r >> 2][r & 3]);
+      if (__ballot(top > mref + slack)) {
+        top = fmaxf(top, __shfl_xor(top, 16, kWave));
+        top = fmaxf(top, __shfl_xor(top, 32, kWave));
+        const float m = fmaxf(mref, top);
+        const float corr = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((mref - m) * c);
+        lsum *= corr;
+#pragma unroll
+        for (int db = 0; db < kDb; ++db) acc[db] *= corr;
+        mref = m;
+      }
+      const float mc = mref == -INFINITY ? 0.0f : -mref * c;
+      bf16x8 pf;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r >> 2][r & 3], c, mc));
+        lsum += p;
+        pf[r] = (__bf16)p;
+      }
+#pragma unroll
+      for (int db = 0; db < kDb; ++db) {
+        unsigned char* at = vlds + (vread ^ (32 * db));
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)at);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at + 16 * kRowB));
+        const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        acc[db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pf, acc[db], 0, 0, 0);
+      }
+    }
+  }
+  lsum += __shfl_xor(lsum, 16, kWave);
+  lsum += __shfl_xor(lsum, 32, kWave);
+
+  // the waves' results meet in LDS: [wave][row][HEAD + 4], then m and l
+  constexpr int kPad = HEAD + 4;
+  float* o = reinterpret_cast<float*>(smem);
+  float* ml = o + 4 * 16 * kPad;
+  __syncthreads();
+#pragma unroll
+  for (int db = 0; db < kDb; ++db)
+    *reinterpret_cast<f32x4_t*>(o + (wave * 16 + l16) * kPad + 16 * db + 4 * qd) = acc[db];
+  if (qd == 0) ml[wave * 32 + l16] = mref, ml[wave * 32 + 16 + l16] = lsum;
+  __syncthreads();
+  const int i = threadIdx.x >> 4, d = (threadIdx.x & 15) * (HEAD / 16);
+  float m = ml[i];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) m = fmaxf(m, ml[w * 32 + i]);
+  float l = 0.0f, sum[HEAD / 16] = {};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float mw = ml[w * 32 + i];
+    if (mw == -INFINITY && m != -INFINITY) continue;
+    const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((mw - m) * c);
+    l += f * ml[w * 32 + 16 + i];
+#pragma unroll
+    for (int e = 0; e < HEAD / 16; ++e) sum[e] += f * o[(w * 16 + i) * kPad + d + e];
+  }
+  // thread group i of 16 writes row i; its numbers are lane i's
+  const int b = __shfl(row.b, i, kWave), hq = __shfl(row.hq, i, kWave);
+  const bool on = __shfl((int)live, i, kWave) != 0;
+  if (!on) return;
+  const size_t r = (size_t)b * g.n_q + hq;
+  if (k.stats) {
+    float* out = k.part + ((size_t)split * k.p.rows + r) * HEAD + d;
+#pragma unroll
+    for (int e = 0; e < HEAD / 16; e += 4)
+      *reinterpret_cast<float4*>(out + e) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+    if ((threadIdx.x & 15) == 0)
+      *reinterpret_cast<float2*>(k.stats + 2 * ((size_t)split * k.p.rows + r)) = make_float2(m, l);
+    return;
+  }
+  // all there is: the output itself
+  uint32_t w[HEAD / 32], bad = 0;
+#pragma unroll
+  for (int e = 0; e < HEAD / 32; ++e) {
+    const bf16x2 y = {(__bf16)(sum[2 * e] / l), (__bf16)(sum[2 * e + 1] / l)};
+    w[e] = __builtin_bit_cast(uint32_t, y);
+    bad |= (w[e] & 0x7F807F80u) + 0x00800080u;
+  }
+  uint16_t* out = g.O + r * HEAD + d;
+  if constexpr (HEAD == 128) *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+  else *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  (void)bad;
+}
+
+template <int HEAD>
+__device__ __forceinline__ void again(const DecodeArgs& g, int b, int hq) {
+  const int n = min(max(g.lens[b], 0), g.max_len), kvh = hq / (g.n_q / g.cache.n_kv);
+  const int page_size = g.cache.page_size, shift = __builtin_ctz(page_size);
+  attend<HEAD>(g.Q + (size_t)b * g.q_stride + (size_t)hq * HEAD, n, g.scale,
                [&](int key, const uint16_t*& k, const uint16_t*& v) {
                  const size_t row = key < g.prefix_len ? 0 : (size_t)b * g.table_width;
                  const int page = g.table[row + (key >> shift)];
                  if (page < 0 || page >= g.cache.pages) return;
-                 const size_t at =
-                     (((size_t)page * g.cache.n_kv + kvh) * page_size + (key & (page_size - 1))) * HEAD;
+                 const size_t at = (((size_t)page * g.cache.n_kv + kvh) * page_size + (key & (page_size - 1))) * HEAD;
                  k = g.cache.k + at;
                  v = g.cache.v + at;
                },
-               g.O + ((size_t)b * g.n_q + h) * HEAD);
+               g.O + ((size_t)b * g.n_q + hq) * HEAD);
+}
+
+template <int HEAD>
+constexpr int narrow_lds() {
+  return 4 * 16 * (HEAD + 4) * 4 + 4 * 32 * 4;      // the join is larger than the four V tiles (4 x 32 rows)
+}
+
+template <int HEAD>
+__global__ __launch_bounds__(256, 2) void chunk_kernel(Kernel k) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const DecodeArgs& g = k.g;
+  const DecodePlan& p = k.p;
+  const int l16 = threadIdx.x & 15;
+  int id = blockIdx.x;
+  const int per_tile = g.cache.n_kv * p.p_splits;
+  if (id < per_tile * p.p_tiles) {
+    // prefix: row tile, chunk, key/value head (one chunk's row tiles on one XCD, 8 apart)
+    const int tile = id / per_tile;
+    id -= tile * per_tile;
+    const int split = id / g.cache.n_kv, kvh = id - split * g.cache.n_kv;
+    const int rows = g.B * p.group, i = tile * 16 + l16, r = min(i, rows - 1);
+    const int b = r / p.group;
+    const Row row{b, kvh * p.group + r - b * p.group, min(max(g.lens[b], 0), g.max_len)};
+    const int key0 = split * p.p_chunk, end = min(key0 + p.p_chunk, min(g.prefix_len, g.max_len));
+    narrow_chunk<HEAD>(k, row, i < rows, kvh, g.table, key0, end, split, smem);
+    return;
+  }
+  id -= per_tile * p.p_tiles;
+  // own tokens: chunk, row tile, sequence, key/value head
+  const int kvh = id % g.cache.n_kv;
+  id /= g.cache.n_kv;
+  const int b = id % g.B;
+  id /= g.B;
+  const int tile = id % p.o_tiles, split = id / p.o_tiles;
+  const int n = min(max(g.lens[b], 0), g.max_len);
+  const int key0 = g.prefix_len + split * p.o_chunk, end = min(key0 + p.o_chunk, n);
+  if (k.stats && key0 >= end) return;
+  const int i = tile * 16 + l16;
+  const Row row{b, kvh * p.group + min(i, p.group - 1), n};
+  narrow_chunk<HEAD>(k, row, i < p.group, kvh, g.table + (size_t)b * g.table_width, key0, end, p.p_splits + split, smem);
+}
+
+// One wave per row: joins its chunks.
+template <int HEAD>
+__global__ __launch_bounds__(256) void join_kernel(Kernel k) {
+  const DecodeArgs& g = k.g;
+  const DecodePlan& p = k.p;
+  const size_t r = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= p.rows) return;
+  const int lane = threadIdx.x & 63;
+  const int b = (int)(r / g.n_q), hq = (int)(r - (size_t)b * g.n_q);
+  const int n = min(max(g.lens[b], 0), g.max_len);
+  const int own = n > g.prefix_len ? (n - g.prefix_len + p.o_chunk - 1) / p.o_chunk : 0;
+  const int live = n > 0 ? p.p_splits + own : 0;
+  const float c = g.scale * kLog2e;
+  constexpr int PER = HEAD / 64;
+  float m = -INFINITY;
+  for (int s = lane; s < live; s += 64) m = fmaxf(m, k.stats[2 * ((size_t)s * p.rows + r)]);
+  m = wave_max(m);
+  float l = 0.0f, o[PER] = {};
+  if (m != -INFINITY) {
+    for (int s0 = 0; s0 < live; s0 += 64) {
+      float f = 0.0f;
+      if (s0 + lane < live) {
+        const float2 v = *reinterpret_cast<const float2*>(k.stats + 2 * ((size_t)(s0 + lane) * p.rows + r));
+        f = v.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((v.x - m) * c);
+        l += f == 0.0f ? 0.0f : f * v.y;
+      }
+      const int count = min(64, live - s0);
+#pragma unroll 8
+      for (int s = 0; s < count; ++s) {
+        const float fs = __shfl(f, s, kWave);
+        const float* v = k.part + ((size_t)(s0 + s) * p.rows + r) * HEAD + lane * PER;
+        float x[PER];
+        if constexpr (PER == 2) {
+          const float2 t = *reinterpret_cast<const float2*>(v);
+          x[0] = t.x, x[1] = t.y;
+        } else {
+          x[0] = *v;
+        }
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] += fs == 0.0f ? 0.0f : fs * x[e];
+      }
+    }
+    l = wave_sum(l);
+  }
+  uint32_t bits = 0;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const __bf16 y = (__bf16)(o[e] / l);
+    bits |= (uint32_t)__builtin_bit_cast(uint16_t, y) << (16 * e);
+  }
+  // nothing seen, or an infinity or NaN: once more, key by key
+  const bool bad = ((bits & 0x7F80u) == 0x7F80u) || (PER == 2 && (bits & 0x7F800000u) == 0x7F800000u);
+  if (__ballot(bad) || m == -INFINITY) {
+    again<HEAD>(g, b, hq);
+    return;
+  }
+  if constexpr (PER == 2) *reinterpret_cast<uint32_t*>(g.O + r * HEAD + lane * 2) = bits;
+  else g.O[r * HEAD + lane] = (uint16_t)bits;
+}
+
+DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len) {
+  DecodePlan p{};
+  p.group = n_q / cache.n_kv;
+  p.rows = (size_t)B * n_q;
+  const int prefix = std::min(prefix_len, max_len), own = std::max(0, max_len - prefix_len);
+  auto chunk_of = [](long long keys, long long pairs) {
+    const long long c = (keys * pairs / 1024 + 127) / 128 * 128;
+    return (int)std::min(1024LL, std::max(128LL, c));
+  };
+  if (prefix > 0) {
+    p.p_tiles = (int)(((long long)B * p.group + 15) / 16);
+    p.p_chunk = chunk_of(prefix, (long long)p.p_tiles * cache.n_kv);
+    p.p_splits = (prefix + p.p_chunk - 1) / p.p_chunk;
+  }
+  p.o_tiles = (p.group + 15) / 16;
+  p.o_chunk = chunk_of(own, (long long)B * cache.n_kv * p.o_tiles);
+  p.o_splits = own > 0 ? (own + p.o_chunk - 1) / p.o_chunk : 0;
+  p.splits = p.p_splits + p.o_splits;
+  p.stats_bytes = align_up((size_t)p.splits * p.rows * 8, 256);
+  p.bytes = p.stats_bytes + (size_t)p.splits * p.rows * cache.head * 4;
+  return p;
+}
+
+long long chunk_blocks(const DecodePlan& p, int B, int n_kv) {
+  return (long long)p.p_tiles * p.p_splits * n_kv + (long long)p.o_tiles * p.o_splits * n_kv * B;
 }
 
 }  // namespace
 
-size_t decode_workspace_bytes(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len) { return 0; }
-bool decode_fits(int B, int n_q) { return ((long long)B * n_q + 3) / 4 * 256 <= kGridThreads; }
+size_t decode_workspace_bytes(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len) {
+  return B == 0 ? 0 : plan_decode(B, n_q, cache, max_len, prefix_len).bytes;
+}
 
-int launch_decode_attention(const DecodeArgs& g, hipStream_t st) {
-  const unsigned blocks = (unsigned)(((long long)g.B * g.n_q + 3) / 4);
-  if (g.cache.head == 64) hipLaunchKernelGGL(decode_kernel<64>, dim3(blocks), dim3(256), 0, st, g);
-  else hipLaunchKernelGGL(decode_kernel<128>, dim3(blocks), dim3(256), 0, st, g);
+bool decode_fits(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len) {
+  const DecodePlan p = plan_decode(B, n_q, cache, max_len, prefix_len);
+  return chunk_blocks(p, B, cache.n_kv) * 256 <= kGridThreads && (long long)((p.rows + 3) / 4) * 256 <= kGridThreads;
+}
+
+template <int HEAD>
+static int launch(const DecodeArgs& g, hipStream_t st) {
+  Kernel k{g, plan_decode(g.B, g.n_q, g.cache, g.max_len, g.prefix_len), nullptr, nullptr};
+  k.stats = static_cast<float*>(g.workspace);
+  k.part = reinterpret_cast<float*>(static_cast<char*>(g.workspace) + k.p.stats_bytes);
+  const long long blocks = chunk_blocks(k.p, g.B, g.cache.n_kv);
+  if (blocks > 0)
+    hipLaunchKernelGGL(chunk_kernel<HEAD>, dim3((unsigned)blocks), dim3(256), narrow_lds<HEAD>(), st, k);
+  hipLaunchKernelGGL(join_kernel<HEAD>, dim3((unsigned)((k.p.rows + 3) / 4)), dim3(256), 0, st, k);
   W4_CHECK_LAUNCH();
   return W4_OK;
+}
+
+int launch_decode_attention(const DecodeArgs& g, hipStream_t st) {
+  return g.cache.head == 64 ? launch<64>(g, st) : launch<128>(g, st);
 }
 
 }  // namespace w4

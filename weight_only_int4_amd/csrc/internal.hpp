@@ -245,7 +245,7 @@ struct DecodeArgs {
   uint16_t* O;
   void* workspace;
 };
-bool decode_fits(int B, int n_q);
+bool decode_fits(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len);
 size_t decode_workspace_bytes(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len);
 int launch_decode_attention(const DecodeArgs& g, hipStream_t stream);
 

@@ -128,7 +128,9 @@ int w4_decode_attention(const uint16_t* Q, long long q_stride, int B, int n_q, c
                         float scale, uint16_t* O, void* workspace, size_t* workspace_bytes, void* stream) {
   if (!cache) return W4_ERR_NULL;
   if (int st = check_cache(*cache, n_q)) return st;
-  if (B < 0 || max_len < 0 || prefix_len < 0 || prefix_len % cache->page_size || !decode_fits(B, n_q)) return W4_ERR_SHAPE;
+  if (B < 0 || max_len < 0 || prefix_len < 0 || prefix_len % cache->page_size ||
+      !decode_fits(B, n_q, *cache, max_len, prefix_len))
+    return W4_ERR_SHAPE;
   const size_t need = decode_workspace_bytes(B, n_q, *cache, max_len, prefix_len);
   if (!workspace && workspace_bytes) {
     *workspace_bytes = need;
