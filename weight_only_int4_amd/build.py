@@ -40,7 +40,7 @@ HIPCC_FLAGS = [
 VGPR_ACC_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 # kernels that never touch their accumulators between MFMAs, and need all 512 registers
 # of one wave per SIMD
-ACC_REGISTER_SOURCES = {"mxfp4_gemm.hip", "prompt_attention.hip"}
+ACC_REGISTER_SOURCES = {"mxfp4_gemm.hip"}
 
 
 # the library links nothing beyond the HIP runtime
