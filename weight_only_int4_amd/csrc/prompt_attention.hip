@@ -2,13 +2,15 @@
 //   O_i = sum_{j <= i} p_ij V_j / l_i,  p_ij = exp(scale q_i . k_j - m_i),  l_i = sum_j p_ij
 // in one pass over the keys with a running reference m and sum l.
 //
-// A workgroup of eight waves, two per SIMD, takes 32 queries a wave: 32 tokens of eight heads of a
-// group, 64 of four, 128 of two or 256 of one, as the group size divides, and walks tiles of 64 keys
+// A workgroup of four or eight waves takes 32 queries a wave: 32 tokens of as many heads of a group as
+// the group size lets it, twice, four times, .. as many tokens of fewer heads, and walks tiles of 64 keys
 // that the waves share.  Scores come transposed, S^T = K Q^T (v_mfma_f32_32x32x16_bf16, keys as rows): lane
 // (query l % 32, half h = l / 32) then holds 16 scores of its own query per 32 keys, so that maximum
 // and sum need one exchange between halves, and its p, rounded to bf16, are the operand of
 // O^T += V^T P^T as they stand: step s of 16 keys takes keys 16 s + 4 h + {0..3} and 8 more, and V^T
 // is read in that order by the transposing LDS read.
+#include <type_traits>
+
 #include "attend.hpp"
 #include "gemm_core.hpp"
 
@@ -19,7 +21,6 @@ namespace w4 {
 namespace {
 
 constexpr int kTile = 64;                     // keys of a tile
-constexpr int kWaves = 8;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -77,14 +78,23 @@ __device__ __forceinline__ bool pick_block(const int32_t* offsets, int B, int T,
   return false;
 }
 
-template <int HEAD>
+// lds_copy16 that LDS reads may pass: for copies into slots that nobody reads before the next barrier.
+// The five wait states are what a vector write to the base (v_readfirstlane, where the compiler comes by
+// it that way) needs before a memory instruction reads it: the compiler does not look into the asm.
+__device__ __forceinline__ void lds_copy16_free(uint32_t off, const void* base, uint32_t lds) {
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds));
+}
+
+template <int HEAD, int WAVES>
 struct Prompt {
+  static constexpr int kWaves = WAVES;
+  static constexpr int kKb = kTile / 32;      // 32-key blocks of a tile
   static constexpr int kSteps = HEAD / 16;    // matrix steps of a score
   static constexpr int kDb = HEAD / 32;       // 32-dim blocks of the output
   static constexpr int kRow = HEAD * 2;       // bytes of an LDS row
   static constexpr int kChunks = HEAD / 8;    // 16-byte pieces of a row
   static constexpr int kTileBytes = kTile * kRow;
-  static constexpr int kStages = 3;           // slots, of K and of V
+  static constexpr int kStages = 2;           // slots, of K and of V
   static constexpr int kCopies = kTileBytes / (kWaves * 1024);   // LDS copies (1 KB) of a wave per tile, K or V
   // LDS rows hold their 16-byte pieces exchanged, so that reads meet distinct banks: piece c of
   // row r at c ^ k_swap(r) (score operand: 16 rows, one piece each) or c ^ v_swap(r) (transposing
@@ -93,9 +103,10 @@ struct Prompt {
   static __device__ __forceinline__ int v_swap(int r) { return HEAD == 128 ? (r & 3) * 4 : ((r >> 1) & 1) * 4; }
 };
 
-template <int HEAD>
-__global__ __launch_bounds__(kWaves * 64, 2) void prompt_kernel(PromptArgs g, int heads, int groups) {
-  using C = Prompt<HEAD>;
+template <int HEAD, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 2) void prompt_kernel(PromptArgs g, int heads, int groups) {
+  using C = Prompt<HEAD, WAVES>;
+  constexpr int kWaves = WAVES;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, h = lane >> 5;
@@ -123,24 +134,26 @@ __global__ __launch_bounds__(kWaves * 64, 2) void prompt_kernel(PromptArgs g, in
   const uint16_t* kbase = g.K + (size_t)first * g.k_stride + (size_t)kvh * HEAD;
   const uint16_t* vbase = g.V + (size_t)first * g.v_stride + (size_t)kvh * HEAD;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
-  const uint32_t koff = row0 * kstep + kpiece, voff = row0 * vstep + vpiece;
+  // lane offsets of the copies in a whole tile, and in the sequence's last, whose rows past the end
+  // repeat its last row
   constexpr int kRowsApart = kWaves * kPerCopy;               // rows between a wave's copies
-  auto copy = [&](const uint16_t* base, long long stride, uint32_t step, uint32_t off, uint32_t piece, int t, uint32_t to) {
-    const int kb = t * kTile;
-    const uint16_t* from = base + (size_t)kb * stride;
-    if (kb + kTile <= n) {
+  const int cut = n / kTile, rest = n - 1 - cut * kTile;      // tiles from `cut` on are not whole
+  uint32_t koff[2][C::kCopies], voff[2][C::kCopies];
 #pragma unroll
-      for (int j = 0; j < C::kCopies; ++j)
-        lds_copy16(off, from + (size_t)(j * kRowsApart) * stride, to + j * kWaves * 1024);
-    } else {                                                  // rows past the sequence repeat its last
-#pragma unroll
-      for (int j = 0; j < C::kCopies; ++j)
-        lds_copy16((uint32_t)min(row0 + j * kRowsApart, n - 1 - kb) * step + piece, from, to + j * kWaves * 1024);
-    }
-  };
+  for (int j = 0; j < C::kCopies; ++j) {
+    const int r = row0 + j * kRowsApart, q = min(r, max(rest, 0));
+    koff[0][j] = r * kstep + kpiece, koff[1][j] = q * kstep + kpiece;
+    voff[0][j] = r * vstep + vpiece, voff[1][j] = q * vstep + vpiece;
+  }
   const uint32_t lds_k = lds0 + wave * 1024, lds_v = lds_k + C::kStages * C::kTileBytes;
-  auto copy_k = [&](int t, int slot) { copy(kbase, g.k_stride, kstep, koff, kpiece, t, lds_k + slot * C::kTileBytes); };
-  auto copy_v = [&](int t, int slot) { copy(vbase, g.v_stride, vstep, voff, vpiece, t, lds_v + slot * C::kTileBytes); };
+  auto copy_k = [&](int t, int slot, int j) {
+    lds_copy16_free(t < cut ? koff[0][j] : koff[1][j], kbase + (size_t)(t * kTile) * g.k_stride,
+                    lds_k + slot * C::kTileBytes + j * kWaves * 1024);
+  };
+  auto copy_v = [&](int t, int slot, int j) {
+    lds_copy16_free(t < cut ? voff[0][j] : voff[1][j], vbase + (size_t)(t * kTile) * g.v_stride,
+                    lds_v + slot * C::kTileBytes + j * kWaves * 1024);
+  };
 
   // operand addresses inside a slot; piece 2 st + h (4 db + ..) of the exchanged rows: one bit
   // pattern away from the first
@@ -152,9 +165,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void prompt_kernel(PromptArgs g, in
             8 * (i & 1);
   }
 
-  copy_k(0, 0);
-  copy_k(min(1, tiles - 1), 1);
-  copy_v(0, 0);
+#pragma unroll
+  for (int i = 0; i < C::kStages; ++i)
+#pragma unroll
+    for (int j = 0; j < C::kCopies; ++j) {
+      copy_k(min(i, tiles - 1), i, j);
+      if (i < C::kStages - 1) copy_v(min(i, tiles - 1), i, j);
+    }
   bf16x8 qf[C::kSteps];
   {
     const uint16_t* qp = g.Q + (size_t)(first + min(q0 + l32, n - 1)) * g.q_stride + (size_t)hq * HEAD + 8 * h;
@@ -166,24 +183,19 @@ __global__ __launch_bounds__(kWaves * 64, 2) void prompt_kernel(PromptArgs g, in
 #pragma unroll
   for (int db = 0; db < C::kDb; ++db) acc[db] = f32x16{};
   float mref = -INFINITY, lsum = 0.0f;
-  typedef f32x16 Scores[2];                   // of 32 keys each
+  typedef f32x16 Scores[C::kKb];              // of 32 keys each
   Scores s;
-  auto scores = [&](int slot) {
-    s[0] = f32x16{}, s[1] = f32x16{};
-    const uint32_t base = opaque_vgpr(kaddr + slot * C::kTileBytes);
-#pragma unroll
-    for (int st = 0; st < C::kSteps; ++st)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        const bf16x8 kf = *(lds_bf16x8)(uintptr_t)((base ^ (32 * st)) + kb * 32 * C::kRow);
-        s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[st], s[kb], 0, 0, 0);
-      }
+  auto read_k = [&](uint32_t base, int i) {   // operand of score step i: dims 16 (i / kKb) .., keys 32 (i % kKb) ..
+    return *(lds_bf16x8)(uintptr_t)((base ^ (32 * (i / C::kKb))) + i % C::kKb * 32 * C::kRow);
+  };
+  auto multiply_k = [&](bf16x8 kf, int i) {
+    s[i % C::kKb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i / C::kKb], i < C::kKb ? f32x16{} : s[i % C::kKb], 0, 0, 0);
   };
   // Raises the reference to the tile's largest score.
   auto follow = [&]() {
     float m = s[0][0];
 #pragma unroll
-    for (int r = 1; r < 32; ++r) m = fmaxf(m, s[r >> 4][r & 15]);
+    for (int r = 1; r < 16 * C::kKb; ++r) m = fmaxf(m, s[r >> 4][r & 15]);
     const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
     m = fmaxf(mref, fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1])));
     const float corr = __builtin_amdgcn_exp2f((mref - m) * c);
@@ -193,13 +205,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void prompt_kernel(PromptArgs g, in
     mref = m;
   };
   // p of a tile, as operands, and their sum: of the rounded p, as the product with V has them
-  bf16x8 pf[4];
+  bf16x8 pf[2 * C::kKb];
   const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
   auto weights = [&]() {
     const float mc = -mref * c;
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 2 * C::kKb; ++k)
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const bf16x2 p = {(__bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[k >> 1][8 * (k & 1) + j], c, mc)),
@@ -209,53 +221,67 @@ __global__ __launch_bounds__(kWaves * 64, 2) void prompt_kernel(PromptArgs g, in
       }
     return sum[0] + sum[1];
   };
-  auto values = [&](int slot) {
-    const uint32_t base = opaque_vgpr(vaddr + slot * C::kTileBytes);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int db = 0; db < C::kDb; ++db) {
-        const uint32_t at = (base ^ (64 * db)) + 16 * k * C::kRow;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(uintptr_t)at);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(uintptr_t)(at + 8 * C::kRow));
-        const bf16x8 vf = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[k], acc[db], 0, 0, 0);
-      }
+  auto read_v = [&](uint32_t base, int i) {   // operand of value step i: keys 16 (i / kDb) .., dims 32 (i % kDb) ..
+    const uint32_t at = (base ^ (64 * (i % C::kDb))) + 16 * (i / C::kDb) * C::kRow;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(uintptr_t)at);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(uintptr_t)(at + 8 * C::kRow));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  // The waves of a SIMD, w and w + 4, work in opposite phases: one turns scores into weights on the
-  // vector ALU while the other multiplies (values of its tile, scores of its next).  A barrier ends
-  // each phase; the late waves begin one phase later.  At the start of a weights phase a wave
-  // issues its copies of K of tile t + 2 and V of tile t + 1, whose slots nobody reads any more; they have
-  // to be there at the third barrier from the early waves', the second from the late waves' issue.
-  const bool late = wave >= kWaves / 2;
-  int t = 0, slot = 0, next = 1;              // tile, its slot, the next tile's
-  auto open = [&]() {
-    copy_k(min(t + 2, tiles - 1), 3 - slot - next);
-    copy_v(min(t + 1, tiles - 1), next);
+  auto multiply_v = [&](bf16x8 vf, int i) {
+    acc[i % C::kDb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[i / C::kDb], acc[i % C::kDb], 0, 0, 0);
   };
+  // One barrier a tile, between its weights and its products.  Among the products a wave issues its
+  // copies of K of tile t + 2 and V of tile t + 1, whose slots nobody reads any more behind that barrier; they
+  // have to be there at the next.
+  constexpr int kBatch = 2 * C::kCopies;
+  int t = 0, slot = 0;                        // tile, its slot
   auto turn = [&]() {                         // weights -> products
-    if (!late) wait_vmcnt<2 * C::kCopies>();
+    wait_vmcnt<0>();
     lds_barrier();
   };
-  auto close = [&]() {                        // products -> weights
-    if (late) wait_vmcnt<0>();
-    lds_barrier();
+  auto copies = [&](int i) {                  // copy i of a tile's, first K's, then V's
+    if (i < C::kCopies) copy_k(min(t + 2, tiles - 1), slot, i);
+    else copy_v(min(t + 1, tiles - 1), slot ^ 1, i - C::kCopies);
+  };
+  auto close = [&]() {                        // products -> the next tile's weights
     ++t;
-    const int after = 3 - slot - next;
-    slot = next, next = after;
+    slot ^= 1;
   };
+  // The values of tile t and the scores of the next, in this order: operands are read four matrix
+  // instructions ahead, copies go between.
+  constexpr int kV = 2 * C::kKb * C::kDb, kK = C::kKb * C::kSteps, kAhead = 4;
+  auto products = [&](auto with_values, auto with_scores, int kslot) {
+    constexpr int v0 = with_values ? 0 : kV, end = with_scores ? kV + kK : kV;
+    const uint32_t vbase_lds = opaque_vgpr(vaddr + slot * C::kTileBytes);
+    const uint32_t kbase_lds = opaque_vgpr(kaddr + kslot * C::kTileBytes);
+    bf16x8 ring[kAhead];
+    auto read = [&](int i) {
+      if (i < end) ring[i % kAhead] = i < kV ? read_v(vbase_lds, i) : read_k(kbase_lds, i - kV);
+    };
+#pragma unroll
+    for (int i = v0; i < v0 + kAhead; ++i) read(i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = v0; i < end; ++i) {
+      if (i < kV) multiply_v(ring[i % kAhead], i);
+      else multiply_k(ring[i % kAhead], i - kV);
+      read(i + kAhead);
+      if (with_values && i % 2 == 1 && i / 2 < kBatch) copies(i / 2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
   wait_vmcnt<0>();
   lds_barrier();
-  if (late) lds_barrier();
   if (my_tiles > 0) {
-    scores(0);
+    products(no, yes, 0);
     if (my_tiles > 1) follow();
     // Tiles whose keys all rows see.  The reference is the first tile's maximum and stays while the p
     // of a row sum to less than 2^30: fp32 and bf16 lose nothing by that, and neither the maximum has to be
     // found nor the accumulators to be scaled.  (Values so large that it overflows come out infinite, and are
     // taken up below.)
     while (t < my_tiles - 1) {
-      open();
       float sum = weights();
       if (__ballot(!(sum < 0x1p30f))) {
         asm volatile("");                     // a branch, not both ways and a choice
@@ -264,30 +290,28 @@ __global__ __launch_bounds__(kWaves * 64, 2) void prompt_kernel(PromptArgs g, in
       }
       lsum += sum;
       turn();
-      values(slot);
-      scores(next);
+      products(yes, yes, slot ^ 1);
       close();
     }
     // the tile that the diagonal or the sequence's end crosses
-    open();
     const int end = min(q0 + l32, n - 1) - t * kTile - 4 * h;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < C::kKb; ++kb)
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         if (32 * kb + (r & 3) + 8 * (r >> 2) > end) s[kb][r] = -INFINITY;
     follow();
     lsum += weights();
     turn();
-    values(slot);
+    products(yes, no, 0);
     close();
   }
   while (t < tiles) {
-    open();
     turn();
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) copies(i);
     close();
   }
-  if (!late) lds_barrier();
   wait_vmcnt<0>();                            // copies past the end
   if (my_tiles == 0) return;
 
@@ -329,38 +353,39 @@ __global__ __launch_bounds__(kWaves * 64, 2) void prompt_kernel(PromptArgs g, in
 
 // heads of a group that a workgroup takes: the more there are, the fewer tokens lie between its
 // waves' ends
-int heads_of(int group) { return group % 8 == 0 ? 8 : group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1; }
+int heads_of(int group, int waves) {
+  int heads = waves;
+  while (group % heads) heads >>= 1;
+  return heads;
+}
 
 // query blocks are at most this many (every sequence may have one that is not full)
-long long most_blocks(int T, int B, int heads) { return (long long)T / (kWaves * 32 / heads) + B; }
+long long most_blocks(int T, int B, int heads, int waves) { return (long long)T / (waves * 32 / heads) + B; }
+
+template <int HEAD, int WAVES>
+int launch(const PromptArgs& g, hipStream_t st) {
+  using C = Prompt<HEAD, WAVES>;
+  const int heads = heads_of(g.n_q / g.n_kv, WAVES), groups = g.n_q / heads;
+  hipLaunchKernelGGL((prompt_kernel<HEAD, WAVES>), dim3((unsigned)(most_blocks(g.T, g.B, heads, WAVES) * groups)),
+                     dim3(WAVES * 64), 2 * C::kTileBytes * C::kStages, st, g, heads, groups);
+  W4_CHECK_LAUNCH();
+  return W4_OK;
+}
 
 }  // namespace
 
 size_t prompt_workspace_bytes(int T, int n_q, int n_kv, int head, int B) { return 0; }
 bool prompt_fits(int T, int n_q, int n_kv, int B) {
-  const int heads = heads_of(n_q / n_kv);
-  return most_blocks(T, B, heads) * (n_q / heads) * kWaves * 64 <= kGridThreads;
-}
-
-template <int HEAD>
-static int launch(const PromptArgs& g, hipStream_t st) {
-  const int heads = heads_of(g.n_q / g.n_kv), groups = g.n_q / heads;
-  const size_t lds = 2 * Prompt<HEAD>::kTileBytes * Prompt<HEAD>::kStages;
-  if (lds > 64 * 1024) {
-    if (hipFuncSetAttribute(reinterpret_cast<const void*>(prompt_kernel<HEAD>), hipFuncAttributeMaxDynamicSharedMemorySize,
-                            (int)lds) != hipSuccess) {
-      (void)hipGetLastError();
-      return W4_ERR_HIP;
-    }
-  }
-  hipLaunchKernelGGL(prompt_kernel<HEAD>, dim3((unsigned)(most_blocks(g.T, g.B, heads) * groups)), dim3(kWaves * 64), lds, st, g,
-                     heads, groups);
-  W4_CHECK_LAUNCH();
-  return W4_OK;
+  const int heads = heads_of(n_q / n_kv, 4);
+  return most_blocks(T, B, heads, 4) * (n_q / heads) * 512 <= kGridThreads;
 }
 
 int launch_prompt_attention(const PromptArgs& g, hipStream_t st) {
-  return g.head == 64 ? launch<64>(g, st) : launch<128>(g, st);
+  // eight waves share each key tile, four end sooner where there are few workgroups (8 x 512 tokens of 16
+  // heads: 24.3 us with eight, 21.1 with four; 1 x 8192: 239 and 252)
+  const bool wide = (long long)g.T * g.n_q >= 512 * 256;
+  if (g.head == 64) return wide ? launch<64, 8>(g, st) : launch<64, 4>(g, st);
+  return wide ? launch<128, 8>(g, st) : launch<128, 4>(g, st);
 }
 
 }  // namespace w4
