@@ -2,6 +2,8 @@
 // single-token attention.  See include/w4a16.h for what each computes.
 #pragma once
 
+#include <atomic>
+
 #include "internal.hpp"
 
 namespace w4 {
@@ -35,6 +37,19 @@ __device__ __forceinline__ int find_sequence(const int32_t* offsets, int B, int 
     n = min(step, n - skip);
   }
   return offsets[lo] <= t && t < offsets[lo + 1] ? lo : -1;
+}
+
+// Asks once per device for more than 64 KB of dynamic LDS for a kernel.
+inline int allow_lds(const void* kernel, int bytes, std::atomic<int> (&state)[64]) {
+  if (bytes <= 64 * 1024) return W4_OK;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return W4_ERR_HIP;
+  int done = state[dev].load(std::memory_order_relaxed);
+  if (done == 0) {
+    done = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess ? 1 : -1;
+    state[dev].store(done, std::memory_order_relaxed);
+  }
+  return done == 1 ? W4_OK : W4_ERR_HIP;
 }
 
 }  // namespace w4
