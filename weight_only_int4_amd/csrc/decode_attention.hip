@@ -6,7 +6,7 @@
 // fp32; a second kernel joins a row's chunks: O = sum_c w_c O_c / sum_c w_c l_c, w_c = exp(scale (m_c - max m)).
 // Chunk sizes follow from what the host knows, so a captured graph serves any lengths.
 #include "attend.hpp"
-#include "gemm_core.hpp"
+#include "flash_tile.hpp"
 
 #pragma clang fp contract(off)
 
@@ -14,12 +14,11 @@ namespace w4 {
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kSlack = 8.0f;                // see the prompt kernel: the reference lags the maximum by at most 2^8
+constexpr float kSlack = 8.0f;                // a reference lags the maximum by at most 2^8: fp32 and bf16 lose nothing by it
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
+
+constexpr int kWideRows = 128;                // rows of a prefix tile of four waves
 
 struct DecodePlan {
   int group, wide;            // queries of a key/value head; prefix rows go 128 to a workgroup (else 16)
@@ -100,7 +99,7 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
   const uint32_t vread = tr * kRowB + 16 * (((l16 & 3) >> 1) ^ swap(tr)) + 8 * (l16 & 1);
 
   bf16x8 kf[2][kSteps];
-  uint4 vf[kLoads];
+  u32x4 vf[kLoads];
   int missing = 0, missing_next = 0;          // bits: the tile's 16-key halves that have no page
   Pages pages{table_row, g.table_width, g.cache.pages, 0, 0};
   auto load_tile = [&](int kb) {              // kb < end; keys past the end repeat the last one
@@ -119,7 +118,7 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
 #pragma unroll
       for (int j = 0; j < kLoads / 2; ++j)
         vf[a * (kLoads / 2) + j] =
-            *reinterpret_cast<const uint4*>(vp + (uint32_t)(min(vrow + j * kRowsPer, last) * HEAD + 8 * vpiece));
+            *reinterpret_cast<const u32x4*>(vp + (uint32_t)(min(vrow + j * kRowsPer, last) * HEAD + 8 * vpiece));
     }
   };
   const int first = key0 + wave * 32;
@@ -138,7 +137,7 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
           s[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[a][st], qf[st], s[a], 0, 0, 0);
       }
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) *reinterpret_cast<uint4*>(vlds + vwrite[j]) = vf[j];
+      for (int j = 0; j < kLoads; ++j) *reinterpret_cast<u32x4*>(vlds + vwrite[j]) = vf[j];
       if (kb + 128 < end) load_tile(kb + 128);
       const int last = min(end, row.limit) - kb - 4 * qd;       // keys from here on are not this row's
       if (__ballot(last < 32 - 4 * qd) || missing) {
@@ -234,6 +233,76 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
   (void)bad;
 }
 
+// One chunk of the prefix, keys [key0, end), for up to 128 rows of the batch: four waves of 32 rows
+// that share the key tiles (flash_tile.hpp).
+template <int HEAD>
+__device__ void wide_chunk(const Kernel& k, int tile, int kvh, int key0, int end, int split, unsigned char* smem) {
+  using F = Flash<HEAD, 4>;
+  const DecodeArgs& g = k.g;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+  const int rows = g.B * k.p.group, i = tile * kWideRows + wave * 32 + l32, r = min(i, rows - 1);
+  const int b = r / k.p.group, hq = kvh * k.p.group + r - b * k.p.group;
+  const int limit = min(end, min(max(g.lens[b], 0), g.max_len));
+  const int page_size = g.cache.page_size, shift = __builtin_ctz(page_size);
+  const size_t page_elems = (size_t)g.cache.n_kv * page_size * HEAD, head_off = (size_t)kvh * page_size * HEAD;
+  // the chunk's pages, one per lane (at most 64: 1,024 keys, 16 a page or more)
+  const int entry0 = key0 >> shift, entries = ((end - 1) >> shift) - entry0 + 1;
+  const int held = lane < entries ? g.table[entry0 + lane] : 0;
+  const bool missing = __ballot((unsigned)held >= (unsigned)g.cache.pages && lane < entries) != 0;
+  int least = limit;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) least = min(least, __shfl_xor(least, off, kWave));
+  const int tiles = (end - key0 + kTile - 1) / kTile;
+  const int masked = missing ? 0 : max(__builtin_amdgcn_readfirstlane(least) - key0, 0) / kTile;
+  const int mine = g.cache.pages > 0 && tile * kWideRows + wave * 32 < rows ? tiles : 0;
+
+  F f;
+  f.init(smem, g.scale);
+  f.load_q(g.Q + (size_t)b * g.q_stride + (size_t)hq * HEAD);
+  // Keys past the end and keys without a page are masked; what is copied for them is some other
+  // page's rows, or rows of the same.
+  const int row0 = F::copy_row();
+  const uint32_t koff = (row0 & 15) * F::kRow + F::k_piece(), voff = (row0 & 15) * F::kRow + F::v_piece();
+  auto page_of = [&](int key) {               // of a wave-uniform key of the chunk
+    const int page = __builtin_amdgcn_readlane(held, (key >> shift) - entry0);
+    return (unsigned)page < (unsigned)g.cache.pages ? page : -1;
+  };
+  if (g.cache.pages > 0)
+    f.template walk<true>(
+        tiles, mine, masked,
+        [&](int kv, int t, int j, uint32_t lds) {
+          const int first = key0 + t * kTile + ((wave * F::kPerCopy + j * F::kRowsApart) & ~15);     // 16 keys of one page
+          const int key = min(first, (end - 1) & ~15);
+          const uint16_t* from = (kv ? g.cache.v : g.cache.k) + (size_t)max(page_of(key), 0) * page_elems + head_off +
+                                 (size_t)(key & (page_size - 1)) * HEAD;
+          lds_copy16_free(kv ? voff : koff, from, lds);
+        },
+        [&](int t) {
+          const int last = limit - key0 - t * kTile - 4 * h;
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int key = key0 + t * kTile + 32 * kb + 16 * half;
+              const bool none = key >= end || page_of(key) < 0;
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                if (none || 32 * kb + 16 * half + (q & 3) + 8 * (q >> 2) >= last) f.s[kb][8 * half + q] = -INFINITY;
+            }
+        });
+  if (i >= rows) return;
+  const size_t row = (size_t)split * k.p.rows + (size_t)b * g.n_q + hq;
+  float* out = k.part + row * HEAD + 4 * h;
+#pragma unroll
+  for (int db = 0; db < F::kDb; ++db)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4*>(out + 32 * db + 8 * q) =
+          make_float4(f.acc[db][4 * q], f.acc[db][4 * q + 1], f.acc[db][4 * q + 2], f.acc[db][4 * q + 3]);
+  if (h == 0) *reinterpret_cast<float2*>(k.stats + 2 * row) = make_float2(f.mref, f.lsum);
+}
+
 template <int HEAD>
 __device__ __forceinline__ void again(const DecodeArgs& g, int b, int hq) {
   const int n = min(max(g.lens[b], 0), g.max_len), kvh = hq / (g.n_q / g.cache.n_kv);
@@ -254,6 +323,10 @@ template <int HEAD>
 constexpr int narrow_lds() {
   return 4 * 16 * (HEAD + 4) * 4 + 4 * 32 * 4;      // the join is larger than the four V tiles (4 x 32 rows)
 }
+template <int HEAD>
+constexpr int chunk_lds(bool wide) {
+  return wide ? Flash<HEAD, 4>::kLds : narrow_lds<HEAD>();
+}
 
 template <int HEAD>
 __global__ __launch_bounds__(256, 2) void chunk_kernel(Kernel k) {
@@ -268,10 +341,14 @@ __global__ __launch_bounds__(256, 2) void chunk_kernel(Kernel k) {
     const int tile = id / per_tile;
     id -= tile * per_tile;
     const int split = id / g.cache.n_kv, kvh = id - split * g.cache.n_kv;
+    const int key0 = split * p.p_chunk, end = min(key0 + p.p_chunk, min(g.prefix_len, g.max_len));
+    if (p.wide) {
+      wide_chunk<HEAD>(k, tile, kvh, key0, end, split, smem);
+      return;
+    }
     const int rows = g.B * p.group, i = tile * 16 + l16, r = min(i, rows - 1);
     const int b = r / p.group;
     const Row row{b, kvh * p.group + r - b * p.group, min(max(g.lens[b], 0), g.max_len)};
-    const int key0 = split * p.p_chunk, end = min(key0 + p.p_chunk, min(g.prefix_len, g.max_len));
     narrow_chunk<HEAD>(k, row, i < rows, kvh, g.table, key0, end, split, smem);
     return;
   }
@@ -360,8 +437,12 @@ DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, in
     return (int)std::min(1024LL, std::max(128LL, c));
   };
   if (prefix > 0) {
-    p.p_tiles = (int)(((long long)B * p.group + 15) / 16);
-    p.p_chunk = chunk_of(prefix, (long long)p.p_tiles * cache.n_kv);
+    const long long rows = (long long)B * p.group;
+    p.wide = rows > 64;
+    p.p_tiles = (int)(p.wide ? (rows + kWideRows - 1) / kWideRows : (rows + 15) / 16);
+    // wide: a workgroup per CU where the prefix is long enough for 256 keys each
+    p.p_chunk = p.wide ? (int)std::min(1024LL, std::max(256LL, (prefix * (long long)p.p_tiles * cache.n_kv / 256 + 63) / 64 * 64))
+                       : chunk_of(prefix, (long long)p.p_tiles * cache.n_kv);
     p.p_splits = (prefix + p.p_chunk - 1) / p.p_chunk;
   }
   p.o_tiles = (p.group + 15) / 16;
@@ -395,7 +476,7 @@ static int launch(const DecodeArgs& g, hipStream_t st) {
   k.part = reinterpret_cast<float*>(static_cast<char*>(g.workspace) + k.p.stats_bytes);
   const long long blocks = chunk_blocks(k.p, g.B, g.cache.n_kv);
   if (blocks > 0)
-    hipLaunchKernelGGL(chunk_kernel<HEAD>, dim3((unsigned)blocks), dim3(256), narrow_lds<HEAD>(), st, k);
+    hipLaunchKernelGGL(chunk_kernel<HEAD>, dim3((unsigned)blocks), dim3(256), chunk_lds<HEAD>(k.p.wide), st, k);
   hipLaunchKernelGGL(join_kernel<HEAD>, dim3((unsigned)((k.p.rows + 3) / 4)), dim3(256), 0, st, k);
   W4_CHECK_LAUNCH();
   return W4_OK;
