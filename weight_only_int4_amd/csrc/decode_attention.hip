@@ -21,7 +21,8 @@ typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
 constexpr int kWideRows = 128;                // rows of a prefix tile of four waves
 
 struct DecodePlan {
-  int group, wide;            // queries of a key/value head; prefix rows go 128 to a workgroup (else 16)
+  int group, prefix;          // queries of a key/value head; keys that the batch shares
+  bool wide, direct;          // prefix rows go 128 to a workgroup (else 16); one chunk in all, no second kernel
   int p_chunk, p_splits, p_tiles;    // prefix: keys of a chunk, chunks, row tiles
   int o_chunk, o_splits, o_tiles;    // own tokens
   int splits;
@@ -57,11 +58,28 @@ struct Pages {
   }
 };
 
-// One chunk of keys [key0, end) for up to 16 rows; four waves take its tiles of 32 keys in turn,
+// One row once more, key by key.
+template <int HEAD>
+__device__ __forceinline__ void again(const DecodeArgs& g, int b, int hq) {
+  const int n = min(max(g.lens[b], 0), g.max_len), kvh = hq / (g.n_q / g.cache.n_kv);
+  const int page_size = g.cache.page_size, shift = __builtin_ctz(page_size);
+  attend<HEAD>(g.Q + (size_t)b * g.q_stride + (size_t)hq * HEAD, n, g.scale,
+               [&](int key, const uint16_t*& k, const uint16_t*& v) {
+                 const size_t row = key < g.prefix_len ? 0 : (size_t)b * g.table_width;
+                 const int page = g.table[row + (key >> shift)];
+                 if (page < 0 || page >= g.cache.pages) return;
+                 const size_t at = (((size_t)page * g.cache.n_kv + kvh) * page_size + (key & (page_size - 1))) * HEAD;
+                 k = g.cache.k + at;
+                 v = g.cache.v + at;
+               },
+               g.O + ((size_t)b * g.n_q + hq) * HEAD);
+}
+
+// One chunk of keys [key0, end) for up to 16 rows; the waves take its tiles of 32 keys in turn,
 // each by itself: K straight into registers as the operand of S^T = K Q^T
 // (v_mfma_f32_16x16x32_bf16), V through LDS, from where the transposing read gives the operand of
 // O^T += V^T P^T; the next tile's loads run meanwhile.
-template <int HEAD>
+template <int HEAD, int WAVES>
 __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh, const int32_t* table_row, int key0,
                              int end, int split, unsigned char* smem) {
   constexpr int kSteps = HEAD / 32, kDb = HEAD / 16, kRowB = 2 * HEAD, kChunks = HEAD / 8;
@@ -73,6 +91,9 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
   const size_t page_elems = (size_t)g.cache.n_kv * page_size * HEAD;
   const size_t head_off = (size_t)kvh * page_size * HEAD;
   unsigned char* vlds = smem + wave * 32 * kRowB;
+  const int first = key0 + wave * 32;
+  Pages pages{table_row, g.table_width, g.cache.pages, 0, 0};
+  pages.load(first >> shift);                 // before the length is known: it arrives meanwhile
 
   bf16x8 qf[kSteps];
   {
@@ -101,32 +122,33 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
   bf16x8 kf[2][kSteps];
   u32x4 vf[kLoads];
   int missing = 0, missing_next = 0;          // bits: the tile's 16-key halves that have no page
-  Pages pages{table_row, g.table_width, g.cache.pages, 0, 0};
   auto load_tile = [&](int kb) {              // kb < end; keys past the end repeat the last one
     missing_next = 0;
+    int last[2];
+    size_t at[2];
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      const int k0 = min(kb + 16 * a, (end - 1) & ~15), last = end - 1 - k0;      // last: 0 .. (15 and more)
+      const int k0 = min(kb + 16 * a, (end - 1) & ~15);
+      last[a] = end - 1 - k0;                 // 0 .. (15 and more)
       const int page = pages(k0 >> shift);
       if (page < 0) missing_next |= 1 << a;
-      const size_t at = (size_t)max(page, 0) * page_elems + head_off + (size_t)(k0 & (page_size - 1)) * HEAD;
-      const uint16_t* kp = g.cache.k + at;
-      const uint16_t* vp = g.cache.v + at;
+      at[a] = (size_t)max(page, 0) * page_elems + head_off + (size_t)(k0 & (page_size - 1)) * HEAD;
 #pragma unroll
       for (int st = 0; st < kSteps; ++st)
-        kf[a][st] = *reinterpret_cast<const bf16x8*>(kp + (uint32_t)(min(l16, last) * HEAD + 32 * st + 8 * qd));
+        kf[a][st] = *reinterpret_cast<const bf16x8*>(g.cache.k + at[a] +
+                                                     (uint32_t)(min(l16, last[a]) * HEAD + 32 * st + 8 * qd));
+    }
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int j = 0; j < kLoads / 2; ++j)
-        vf[a * (kLoads / 2) + j] =
-            *reinterpret_cast<const u32x4*>(vp + (uint32_t)(min(vrow + j * kRowsPer, last) * HEAD + 8 * vpiece));
-    }
+        vf[a * (kLoads / 2) + j] = *reinterpret_cast<const u32x4*>(
+            g.cache.v + at[a] + (uint32_t)(min(vrow + j * kRowsPer, last[a]) * HEAD + 8 * vpiece));
   };
-  const int first = key0 + wave * 32;
   const bool work = first < end && g.cache.pages > 0;
   if (work) {
-    pages.load(first >> shift);
     load_tile(first);
-    for (int kb = first; kb < end; kb += 128) {
+    for (int kb = first; kb < end; kb += 32 * WAVES) {
       missing = missing_next;
       f32x4_t s[2];
 #pragma unroll
@@ -138,7 +160,7 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
       }
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) *reinterpret_cast<u32x4*>(vlds + vwrite[j]) = vf[j];
-      if (kb + 128 < end) load_tile(kb + 128);
+      if (kb + 32 * WAVES < end) load_tile(kb + 32 * WAVES);
       const int last = min(end, row.limit) - kb - 4 * qd;       // keys from here on are not this row's
       if (__ballot(last < 32 - 4 * qd) || missing) {
 #pragma unroll
@@ -184,20 +206,21 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
   // the waves' results meet in LDS: [wave][row][HEAD + 4], then m and l
   constexpr int kPad = HEAD + 4;
   float* o = reinterpret_cast<float*>(smem);
-  float* ml = o + 4 * 16 * kPad;
+  float* ml = o + WAVES * 16 * kPad;
   __syncthreads();
 #pragma unroll
   for (int db = 0; db < kDb; ++db)
     *reinterpret_cast<f32x4_t*>(o + (wave * 16 + l16) * kPad + 16 * db + 4 * qd) = acc[db];
   if (qd == 0) ml[wave * 32 + l16] = mref, ml[wave * 32 + 16 + l16] = lsum;
   __syncthreads();
+  if (threadIdx.x >= 256) return;
   const int i = threadIdx.x >> 4, d = (threadIdx.x & 15) * (HEAD / 16);
   float m = ml[i];
 #pragma unroll
-  for (int w = 1; w < 4; ++w) m = fmaxf(m, ml[w * 32 + i]);
+  for (int w = 1; w < WAVES; ++w) m = fmaxf(m, ml[w * 32 + i]);
   float l = 0.0f, sum[HEAD / 16] = {};
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     const float mw = ml[w * 32 + i];
     if (mw == -INFINITY && m != -INFINITY) continue;
     const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((mw - m) * c);
@@ -208,9 +231,9 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
   // thread group i of 16 writes row i; its numbers are lane i's
   const int b = __shfl(row.b, i, kWave), hq = __shfl(row.hq, i, kWave);
   const bool on = __shfl((int)live, i, kWave) != 0;
-  if (!on) return;
   const size_t r = (size_t)b * g.n_q + hq;
   if (k.stats) {
+    if (!on) return;
     float* out = k.part + ((size_t)split * k.p.rows + r) * HEAD + d;
 #pragma unroll
     for (int e = 0; e < HEAD / 16; e += 4)
@@ -219,18 +242,23 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
       *reinterpret_cast<float2*>(k.stats + 2 * ((size_t)split * k.p.rows + r)) = make_float2(m, l);
     return;
   }
-  // all there is: the output itself
-  uint32_t w[HEAD / 32], bad = 0;
+  // all there is: the output itself; rows that see nothing, or that are not finite, once more, key by key
+  uint32_t w[HEAD / 32], bad = on && m == -INFINITY ? 0x80008000u : 0u;
 #pragma unroll
   for (int e = 0; e < HEAD / 32; ++e) {
     const bf16x2 y = {(__bf16)(sum[2 * e] / l), (__bf16)(sum[2 * e + 1] / l)};
     w[e] = __builtin_bit_cast(uint32_t, y);
-    bad |= (w[e] & 0x7F807F80u) + 0x00800080u;
+    bad |= on ? (w[e] & 0x7F807F80u) + 0x00800080u : 0u;
   }
   uint16_t* out = g.O + r * HEAD + d;
-  if constexpr (HEAD == 128) *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-  else *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-  (void)bad;
+  if (on) {
+    if constexpr (HEAD == 128) *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  }
+  const unsigned long long rows = __ballot((bad & 0x80008000u) != 0);
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j)                 // a wave's four rows, 16 lanes each
+    if (rows >> (16 * j) & 0xFFFF) again<HEAD>(g, __shfl(b, 16 * j, kWave), __shfl(hq, 16 * j, kWave));
 }
 
 // One chunk of the prefix, keys [key0, end), for up to 128 rows of the batch: four waves of 32 rows
@@ -303,33 +331,18 @@ __device__ void wide_chunk(const Kernel& k, int tile, int kvh, int key0, int end
   if (h == 0) *reinterpret_cast<float2*>(k.stats + 2 * row) = make_float2(f.mref, f.lsum);
 }
 
-template <int HEAD>
-__device__ __forceinline__ void again(const DecodeArgs& g, int b, int hq) {
-  const int n = min(max(g.lens[b], 0), g.max_len), kvh = hq / (g.n_q / g.cache.n_kv);
-  const int page_size = g.cache.page_size, shift = __builtin_ctz(page_size);
-  attend<HEAD>(g.Q + (size_t)b * g.q_stride + (size_t)hq * HEAD, n, g.scale,
-               [&](int key, const uint16_t*& k, const uint16_t*& v) {
-                 const size_t row = key < g.prefix_len ? 0 : (size_t)b * g.table_width;
-                 const int page = g.table[row + (key >> shift)];
-                 if (page < 0 || page >= g.cache.pages) return;
-                 const size_t at = (((size_t)page * g.cache.n_kv + kvh) * page_size + (key & (page_size - 1))) * HEAD;
-                 k = g.cache.k + at;
-                 v = g.cache.v + at;
-               },
-               g.O + ((size_t)b * g.n_q + hq) * HEAD);
-}
-
-template <int HEAD>
+template <int HEAD, int WAVES>
 constexpr int narrow_lds() {
-  return 4 * 16 * (HEAD + 4) * 4 + 4 * 32 * 4;      // the join is larger than the four V tiles (4 x 32 rows)
-}
-template <int HEAD>
-constexpr int chunk_lds(bool wide) {
-  return wide ? Flash<HEAD, 4>::kLds : narrow_lds<HEAD>();
+  return WAVES * 16 * (HEAD + 4) * 4 + WAVES * 32 * 4;     // the join is larger than the V tiles (32 rows a wave)
 }
 
-template <int HEAD>
-__global__ __launch_bounds__(256, 2) void chunk_kernel(Kernel k) {
+template <int HEAD, int WAVES, bool WIDE>
+constexpr int chunk_lds() {
+  return WIDE ? std::max(Flash<HEAD, 4>::kLds, narrow_lds<HEAD, WAVES>()) : narrow_lds<HEAD, WAVES>();
+}
+
+template <int HEAD, int WAVES, bool WIDE>
+__global__ __launch_bounds__(WAVES * 64, 2) void chunk_kernel(Kernel k) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const DecodeArgs& g = k.g;
   const DecodePlan& p = k.p;
@@ -341,15 +354,15 @@ __global__ __launch_bounds__(256, 2) void chunk_kernel(Kernel k) {
     const int tile = id / per_tile;
     id -= tile * per_tile;
     const int split = id / g.cache.n_kv, kvh = id - split * g.cache.n_kv;
-    const int key0 = split * p.p_chunk, end = min(key0 + p.p_chunk, min(g.prefix_len, g.max_len));
-    if (p.wide) {
+    const int key0 = split * p.p_chunk, end = min(key0 + p.p_chunk, p.prefix);
+    if constexpr (WIDE) {
       wide_chunk<HEAD>(k, tile, kvh, key0, end, split, smem);
-      return;
+    } else {
+      const int rows = g.B * p.group, i = tile * 16 + l16, r = min(i, rows - 1);
+      const int b = r / p.group;
+      const Row row{b, kvh * p.group + r - b * p.group, min(max(g.lens[b], 0), g.max_len)};
+      narrow_chunk<HEAD, WAVES>(k, row, i < rows, kvh, g.table, key0, end, split, smem);
     }
-    const int rows = g.B * p.group, i = tile * 16 + l16, r = min(i, rows - 1);
-    const int b = r / p.group;
-    const Row row{b, kvh * p.group + r - b * p.group, min(max(g.lens[b], 0), g.max_len)};
-    narrow_chunk<HEAD>(k, row, i < rows, kvh, g.table, key0, end, split, smem);
     return;
   }
   id -= per_tile * p.p_tiles;
@@ -360,31 +373,32 @@ __global__ __launch_bounds__(256, 2) void chunk_kernel(Kernel k) {
   id /= g.B;
   const int tile = id % p.o_tiles, split = id / p.o_tiles;
   const int n = min(max(g.lens[b], 0), g.max_len);
-  const int key0 = g.prefix_len + split * p.o_chunk, end = min(key0 + p.o_chunk, n);
+  const int key0 = p.prefix + split * p.o_chunk, end = min(key0 + p.o_chunk, n);
   if (k.stats && key0 >= end) return;
   const int i = tile * 16 + l16;
   const Row row{b, kvh * p.group + min(i, p.group - 1), n};
-  narrow_chunk<HEAD>(k, row, i < p.group, kvh, g.table + (size_t)b * g.table_width, key0, end, p.p_splits + split, smem);
+  narrow_chunk<HEAD, WAVES>(k, row, i < p.group, kvh, g.table + (size_t)b * g.table_width, key0, end, p.p_splits + split, smem);
 }
 
-// One wave per row: joins its chunks.
+// One wave per row: joins its chunks, 16 bytes a lane, so that 64 / (head / 4) chunks are read at once.
 template <int HEAD>
 __global__ __launch_bounds__(256) void join_kernel(Kernel k) {
+  constexpr int kLanes = HEAD / 4, kAtOnce = 64 / kLanes;
   const DecodeArgs& g = k.g;
   const DecodePlan& p = k.p;
   const size_t r = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (r >= p.rows) return;
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, sub = lane / kLanes, d = 4 * (lane % kLanes);
   const int b = (int)(r / g.n_q), hq = (int)(r - (size_t)b * g.n_q);
   const int n = min(max(g.lens[b], 0), g.max_len);
-  const int own = n > g.prefix_len ? (n - g.prefix_len + p.o_chunk - 1) / p.o_chunk : 0;
+  const int own = n > p.prefix ? (n - p.prefix + p.o_chunk - 1) / p.o_chunk : 0;
   const int live = n > 0 ? p.p_splits + own : 0;
   const float c = g.scale * kLog2e;
-  constexpr int PER = HEAD / 64;
   float m = -INFINITY;
   for (int s = lane; s < live; s += 64) m = fmaxf(m, k.stats[2 * ((size_t)s * p.rows + r)]);
   m = wave_max(m);
-  float l = 0.0f, o[PER] = {};
+  float l = 0.0f;
+  f32x4_t o = {};
   if (m != -INFINITY) {
     for (int s0 = 0; s0 < live; s0 += 64) {
       float f = 0.0f;
@@ -394,60 +408,71 @@ __global__ __launch_bounds__(256) void join_kernel(Kernel k) {
         l += f == 0.0f ? 0.0f : f * v.y;
       }
       const int count = min(64, live - s0);
-#pragma unroll 8
-      for (int s = 0; s < count; ++s) {
-        const float fs = __shfl(f, s, kWave);
-        const float* v = k.part + ((size_t)(s0 + s) * p.rows + r) * HEAD + lane * PER;
-        float x[PER];
-        if constexpr (PER == 2) {
-          const float2 t = *reinterpret_cast<const float2*>(v);
-          x[0] = t.x, x[1] = t.y;
-        } else {
-          x[0] = *v;
+      for (int s1 = 0; s1 < count; s1 += 8 * kAtOnce) {
+        f32x4_t x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int s = min(s1 + u * kAtOnce + sub, count - 1);
+          x[u] = *reinterpret_cast<const f32x4_t*>(k.part + ((size_t)(s0 + s) * p.rows + r) * HEAD + d);
         }
 #pragma unroll
-        for (int e = 0; e < PER; ++e) o[e] += fs == 0.0f ? 0.0f : fs * x[e];
+        for (int u = 0; u < 8; ++u) {
+          const int s = s1 + u * kAtOnce + sub;
+          const float fs = __shfl(f, min(s, 63), kWave);
+          if (s < count && fs != 0.0f) o += fs * x[u];       // (a chunk of weight 0 may hold anything)
+        }
       }
     }
     l = wave_sum(l);
   }
-  uint32_t bits = 0;
 #pragma unroll
-  for (int e = 0; e < PER; ++e) {
-    const __bf16 y = (__bf16)(o[e] / l);
-    bits |= (uint32_t)__builtin_bit_cast(uint16_t, y) << (16 * e);
-  }
+  for (int off = kLanes; off < 64; off *= 2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], off, kWave);
+  const bf16x2 y0 = {(__bf16)(o[0] / l), (__bf16)(o[1] / l)}, y1 = {(__bf16)(o[2] / l), (__bf16)(o[3] / l)};
+  const uint2 w = make_uint2(__builtin_bit_cast(uint32_t, y0), __builtin_bit_cast(uint32_t, y1));
   // nothing seen, or an infinity or NaN: once more, key by key
-  const bool bad = ((bits & 0x7F80u) == 0x7F80u) || (PER == 2 && (bits & 0x7F800000u) == 0x7F800000u);
-  if (__ballot(bad) || m == -INFINITY) {
+  const uint32_t bad = ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u);
+  if (m == -INFINITY || __ballot((bad & 0x80008000u) != 0)) {
     again<HEAD>(g, b, hq);
     return;
   }
-  if constexpr (PER == 2) *reinterpret_cast<uint32_t*>(g.O + r * HEAD + lane * 2) = bits;
-  else g.O[r * HEAD + lane] = (uint16_t)bits;
+  if (sub == 0) *reinterpret_cast<uint2*>(g.O + r * HEAD + d) = w;
 }
+
+// Two workgroups a CU are one round: chunks are as long as that asks for (512 workgroups), between 128
+// keys (four waves' tiles) and 1,024.
+int chunk_of(long long work) { return (int)std::min(1024LL, std::max(128LL, (work / 512 + 127) / 128 * 128)); }
 
 DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len) {
   DecodePlan p{};
   p.group = n_q / cache.n_kv;
   p.rows = (size_t)B * n_q;
-  const int prefix = std::min(prefix_len, max_len), own = std::max(0, max_len - prefix_len);
-  auto chunk_of = [](long long keys, long long pairs) {
-    const long long c = (keys * pairs / 1024 + 127) / 128 * 128;
-    return (int)std::min(1024LL, std::max(128LL, c));
-  };
-  if (prefix > 0) {
+  p.prefix = B > 1 ? std::min(prefix_len, max_len) : 0;      // (a single sequence shares with nobody)
+  const int own = max_len - p.prefix;
+  p.o_tiles = (p.group + 15) / 16;
+  if (p.prefix == 0 && own <= 1024) {
+    p.direct = true;
+    p.o_chunk = 1024, p.o_splits = p.splits = 1;
+    return p;
+  }
+  const long long o_work = (long long)own * B * cache.n_kv * p.o_tiles;
+  if (p.prefix > 0) {
     const long long rows = (long long)B * p.group;
     p.wide = rows > 64;
     p.p_tiles = (int)(p.wide ? (rows + kWideRows - 1) / kWideRows : (rows + 15) / 16);
-    // wide: a workgroup per CU where the prefix is long enough for 256 keys each
-    p.p_chunk = p.wide ? (int)std::min(1024LL, std::max(256LL, (prefix * (long long)p.p_tiles * cache.n_kv / 256 + 63) / 64 * 64))
-                       : chunk_of(prefix, (long long)p.p_tiles * cache.n_kv);
-    p.p_splits = (prefix + p.p_chunk - 1) / p.p_chunk;
+    const long long p_work = (long long)p.prefix * p.p_tiles * cache.n_kv;
+    // wide: a workgroup per CU, or as long a walk as goes along with half the time that the own tokens take to
+    // read (a tile of 64 keys takes 1.3 us, a CU's share of the memory's rate is about 18 GB/s)
+    const long long along = o_work / p.o_tiles * cache.head / 45000;
+    p.p_chunk = p.wide ? (int)std::min(1024LL, std::max(256LL, (std::max(p_work / 256, along) + 63) / 64 * 64))
+                       : chunk_of(p_work + o_work);
+    p.o_chunk = p.wide ? chunk_of(o_work) : p.p_chunk;
+    p.p_splits = (p.prefix + p.p_chunk - 1) / p.p_chunk;
+  } else {
+    p.o_chunk = chunk_of(o_work);
   }
-  p.o_tiles = (p.group + 15) / 16;
-  p.o_chunk = chunk_of(own, (long long)B * cache.n_kv * p.o_tiles);
-  p.o_splits = own > 0 ? (own + p.o_chunk - 1) / p.o_chunk : 0;
+  p.o_splits = (own + p.o_chunk - 1) / p.o_chunk;
   p.splits = p.p_splits + p.o_splits;
   p.stats_bytes = align_up((size_t)p.splits * p.rows * 8, 256);
   p.bytes = p.stats_bytes + (size_t)p.splits * p.rows * cache.head * 4;
@@ -466,18 +491,32 @@ size_t decode_workspace_bytes(int B, int n_q, const w4_kv_cache& cache, int max_
 
 bool decode_fits(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len) {
   const DecodePlan p = plan_decode(B, n_q, cache, max_len, prefix_len);
-  return chunk_blocks(p, B, cache.n_kv) * 256 <= kGridThreads && (long long)((p.rows + 3) / 4) * 256 <= kGridThreads;
+  return chunk_blocks(p, B, cache.n_kv) * 512 <= kGridThreads && (long long)((p.rows + 3) / 4) * 256 <= kGridThreads;
+}
+
+template <int HEAD, int WAVES, bool WIDE>
+static int launch_chunks(const Kernel& k, hipStream_t st) {
+  const long long blocks = chunk_blocks(k.p, k.g.B, k.g.cache.n_kv);
+  constexpr int kLds = chunk_lds<HEAD, WAVES, WIDE>();
+  static std::atomic<int> state[64];          // 0 not yet, 1 done, -1 failed (per device)
+  if (int rc = allow_lds(reinterpret_cast<const void*>(chunk_kernel<HEAD, WAVES, WIDE>), kLds, state)) return rc;
+  hipLaunchKernelGGL((chunk_kernel<HEAD, WAVES, WIDE>), dim3((unsigned)blocks), dim3(WAVES * 64), kLds, st, k);
+  return W4_OK;
 }
 
 template <int HEAD>
 static int launch(const DecodeArgs& g, hipStream_t st) {
   Kernel k{g, plan_decode(g.B, g.n_q, g.cache, g.max_len, g.prefix_len), nullptr, nullptr};
-  k.stats = static_cast<float*>(g.workspace);
-  k.part = reinterpret_cast<float*>(static_cast<char*>(g.workspace) + k.p.stats_bytes);
-  const long long blocks = chunk_blocks(k.p, g.B, g.cache.n_kv);
-  if (blocks > 0)
-    hipLaunchKernelGGL(chunk_kernel<HEAD>, dim3((unsigned)blocks), dim3(256), chunk_lds<HEAD>(k.p.wide), st, k);
-  hipLaunchKernelGGL(join_kernel<HEAD>, dim3((unsigned)((k.p.rows + 3) / 4)), dim3(256), 0, st, k);
+  if (!k.p.direct) {
+    k.stats = static_cast<float*>(g.workspace);
+    k.part = reinterpret_cast<float*>(static_cast<char*>(g.workspace) + k.p.stats_bytes);
+  }
+  if (int rc = k.p.direct ? launch_chunks<HEAD, 8, false>(k, st)
+               : k.p.wide ? launch_chunks<HEAD, 4, true>(k, st)
+                          : launch_chunks<HEAD, 4, false>(k, st))
+    return rc;
+  if (!k.p.direct)
+    hipLaunchKernelGGL(join_kernel<HEAD>, dim3((unsigned)((k.p.rows + 3) / 4)), dim3(256), 0, st, k);
   W4_CHECK_LAUNCH();
   return W4_OK;
 }
