@@ -41,22 +41,22 @@ struct Kernel {
   float* part;
 };
 
-// Page numbers of 64 table entries, one per lane; a lane index past them moves the window.
+// Page numbers of the 64 table entries from `base` on, one per lane: 1,024 keys, 16 a page or more.
 struct Pages {
-  const int32_t* row;
-  int width, pages, base, held;
-  __device__ __forceinline__ void load(int entry) {
-    const int e = entry + (threadIdx.x & 63);
-    base = entry;
+  int pages, base, held;
+  __device__ __forceinline__ Pages(const int32_t* row, int width, int pages, int base) : pages(pages), base(base) {
+    const int e = base + (threadIdx.x & 63);
     held = e < width ? row[e] : -1;
   }
   // page of a (wave-uniform) entry, -1 if there is none
-  __device__ __forceinline__ int operator()(int entry) {
-    if (entry - base >= 64) load(entry);
+  __device__ __forceinline__ int operator()(int entry) const {
     const int page = __builtin_amdgcn_readlane(held, entry - base);
     return (unsigned)page < (unsigned)pages ? page : -1;
   }
 };
+
+typedef const __attribute__((address_space(1))) char* global_bytes;
+typedef const __attribute__((address_space(1))) u32x4* global_u32x4;
 
 // One row once more, key by key.
 template <int HEAD>
@@ -92,8 +92,7 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
   const size_t head_off = (size_t)kvh * page_size * HEAD;
   unsigned char* vlds = smem + wave * 32 * kRowB;
   const int first = key0 + wave * 32;
-  Pages pages{table_row, g.table_width, g.cache.pages, 0, 0};
-  pages.load(first >> shift);                 // before the length is known: it arrives meanwhile
+  const Pages pages(table_row, g.table_width, g.cache.pages, first >> shift);     // before the length is known
 
   bf16x8 qf[kSteps];
   {
@@ -101,7 +100,7 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) qf[st] = *reinterpret_cast<const bf16x8*>(qp + 32 * st);
   }
-  const float c = g.scale * kLog2e, slack = kSlack / c;
+  const float c = g.scale * kLog2e;
   f32x4_t acc[kDb];
 #pragma unroll
   for (int db = 0; db < kDb; ++db) acc[db] = f32x4_t{};
@@ -122,28 +121,35 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
   bf16x8 kf[2][kSteps];
   u32x4 vf[kLoads];
   int missing = 0, missing_next = 0;          // bits: the tile's 16-key halves that have no page
-  auto load_tile = [&](int kb) {              // kb < end; keys past the end repeat the last one
+  // byte offsets into 16 rows of a page; the chunk's last 16 may end early: their rows past the end
+  // repeat the last one in V (K's scores are masked)
+  const uint32_t koff = l16 * kRowB + 16 * qd, voff = vrow * kRowB + 16 * vpiece;
+  const int final16 = (end - 1) & ~15;
+  uint32_t vfinal[kLoads / 2];
+#pragma unroll
+  for (int j = 0; j < kLoads / 2; ++j) vfinal[j] = min(vrow + j * kRowsPer, (end - 1) & 15) * kRowB + 16 * vpiece;
+  auto load_tile = [&](int kb) {              // kb < end
     missing_next = 0;
-    int last[2];
-    size_t at[2];
+    global_bytes kp[2], vp[2];
+    bool final_half[2];
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      const int k0 = min(kb + 16 * a, (end - 1) & ~15);
-      last[a] = end - 1 - k0;                 // 0 .. (15 and more)
+      const int k0 = min(kb + 16 * a, final16);
+      final_half[a] = k0 == final16;
       const int page = pages(k0 >> shift);
       if (page < 0) missing_next |= 1 << a;
-      at[a] = (size_t)max(page, 0) * page_elems + head_off + (size_t)(k0 & (page_size - 1)) * HEAD;
+      const size_t at = 2 * ((size_t)max(page, 0) * page_elems + head_off + (size_t)(k0 & (page_size - 1)) * HEAD);
+      kp[a] = (global_bytes)g.cache.k + at;
+      vp[a] = (global_bytes)g.cache.v + at;
 #pragma unroll
       for (int st = 0; st < kSteps; ++st)
-        kf[a][st] = *reinterpret_cast<const bf16x8*>(g.cache.k + at[a] +
-                                                     (uint32_t)(min(l16, last[a]) * HEAD + 32 * st + 8 * qd));
+        kf[a][st] = __builtin_bit_cast(bf16x8, *(global_u32x4)(kp[a] + (koff + 64 * st)));
     }
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int j = 0; j < kLoads / 2; ++j)
-        vf[a * (kLoads / 2) + j] = *reinterpret_cast<const u32x4*>(
-            g.cache.v + at[a] + (uint32_t)(min(vrow + j * kRowsPer, last[a]) * HEAD + 8 * vpiece));
+        vf[a * (kLoads / 2) + j] = *(global_u32x4)(vp[a] + (final_half[a] ? vfinal[j] : voff + j * kRowsPer * kRowB));
   };
   const bool work = first < end && g.cache.pages > 0;
   if (work) {
@@ -172,7 +178,7 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
       float top = s[0][0];
 #pragma unroll
       for (int r = 1; r < 8; ++r) top = fmaxf(top, s[r >> 2][r & 3]);
-      if (__ballot(top > mref + slack)) {
+      if (__ballot((top - mref) * c > kSlack)) {
         top = fmaxf(top, __shfl_xor(top, 16, kWave));
         top = fmaxf(top, __shfl_xor(top, 32, kWave));
         const float m = fmaxf(mref, top);
