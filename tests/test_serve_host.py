@@ -2,6 +2,8 @@
 and the entry points' refusals."""
 import ctypes
 import math
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -111,6 +113,15 @@ def test_append_places_tokens():
     assert np.array_equal(qo[3], q[3]) and np.array_equal(vc[1, :, 0], v[3]) and np.array_equal(vc[1, :, 1], v[4])
     assert np.array_equal(kc[0, :, 0], SO.rotate(k[:1], cs[16:17], sn[16:17])[0])
     assert (kc != 9).any(axis=(1, 3)).sum() == 4
+
+
+def test_what_device_arrays_say_is_held_in_range(tmp_path):
+    """The kernels' own functions for offsets, lengths, positions and page numbers, compiled for the host."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = str(tmp_path / "held_check")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-o", exe, os.path.join(here, "held_check.cpp")], check=True)
+    res = subprocess.run([exe], capture_output=True, text=True)
+    assert res.returncode == 0, res.stdout
 
 
 # ---------------------------------------------------------------- refusals of the C entry points

@@ -50,8 +50,7 @@ struct Pages {
   }
   // page of a (wave-uniform) entry, -1 if there is none
   __device__ __forceinline__ int operator()(int entry) const {
-    const int page = __builtin_amdgcn_readlane(held, entry - base);
-    return (unsigned)page < (unsigned)pages ? page : -1;
+    return held_page(__builtin_amdgcn_readlane(held, entry - base), pages);
   }
 };
 
@@ -61,13 +60,13 @@ typedef const __attribute__((address_space(1))) u32x4* global_u32x4;
 // One row once more, key by key.
 template <int HEAD>
 __device__ __forceinline__ void again(const DecodeArgs& g, int b, int hq) {
-  const int n = min(max(g.lens[b], 0), g.max_len), kvh = hq / (g.n_q / g.cache.n_kv);
+  const int n = held_length(g.lens[b], g.max_len), kvh = hq / (g.n_q / g.cache.n_kv);
   const int page_size = g.cache.page_size, shift = __builtin_ctz(page_size);
   attend<HEAD>(g.Q + (size_t)b * g.q_stride + (size_t)hq * HEAD, n, g.scale,
                [&](int key, const uint16_t*& k, const uint16_t*& v) {
                  const size_t row = key < g.prefix_len ? 0 : (size_t)b * g.table_width;
-                 const int page = g.table[row + (key >> shift)];
-                 if (page < 0 || page >= g.cache.pages) return;
+                 const int page = held_page(g.table[row + (key >> shift)], g.cache.pages);
+                 if (page < 0) return;
                  const size_t at = (((size_t)page * g.cache.n_kv + kvh) * page_size + (key & (page_size - 1))) * HEAD;
                  k = g.cache.k + at;
                  v = g.cache.v + at;
@@ -277,13 +276,13 @@ __device__ void wide_chunk(const Kernel& k, int tile, int kvh, int key0, int end
   const int l32 = lane & 31, h = lane >> 5;
   const int rows = g.B * k.p.group, i = tile * kWideRows + wave * 32 + l32, r = min(i, rows - 1);
   const int b = r / k.p.group, hq = kvh * k.p.group + r - b * k.p.group;
-  const int limit = min(end, min(max(g.lens[b], 0), g.max_len));
+  const int limit = min(end, held_length(g.lens[b], g.max_len));
   const int page_size = g.cache.page_size, shift = __builtin_ctz(page_size);
   const size_t page_elems = (size_t)g.cache.n_kv * page_size * HEAD, head_off = (size_t)kvh * page_size * HEAD;
   // the chunk's pages, one per lane (at most 64: 1,024 keys, 16 a page or more)
   const int entry0 = key0 >> shift, entries = ((end - 1) >> shift) - entry0 + 1;
   const int held = lane < entries ? g.table[entry0 + lane] : 0;
-  const bool missing = __ballot((unsigned)held >= (unsigned)g.cache.pages && lane < entries) != 0;
+  const bool missing = __ballot(lane < entries && held_page(held, g.cache.pages) < 0) != 0;
   int least = limit;
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) least = min(least, __shfl_xor(least, off, kWave));
@@ -299,8 +298,7 @@ __device__ void wide_chunk(const Kernel& k, int tile, int kvh, int key0, int end
   const int row0 = F::copy_row();
   const uint32_t koff = (row0 & 15) * F::kRow + F::k_piece(), voff = (row0 & 15) * F::kRow + F::v_piece();
   auto page_of = [&](int key) {               // of a wave-uniform key of the chunk
-    const int page = __builtin_amdgcn_readlane(held, (key >> shift) - entry0);
-    return (unsigned)page < (unsigned)g.cache.pages ? page : -1;
+    return held_page(__builtin_amdgcn_readlane(held, (key >> shift) - entry0), g.cache.pages);
   };
   if (g.cache.pages > 0)
     f.template walk<true>(
@@ -366,7 +364,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void chunk_kernel(Kernel k) {
     } else {
       const int rows = g.B * p.group, i = tile * 16 + l16, r = min(i, rows - 1);
       const int b = r / p.group;
-      const Row row{b, kvh * p.group + r - b * p.group, min(max(g.lens[b], 0), g.max_len)};
+      const Row row{b, kvh * p.group + r - b * p.group, held_length(g.lens[b], g.max_len)};
       narrow_chunk<HEAD, WAVES>(k, row, i < rows, kvh, g.table, key0, end, split, smem);
     }
     return;
@@ -378,7 +376,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void chunk_kernel(Kernel k) {
   const int b = id % g.B;
   id /= g.B;
   const int tile = id % p.o_tiles, split = id / p.o_tiles;
-  const int n = min(max(g.lens[b], 0), g.max_len);
+  const int n = held_length(g.lens[b], g.max_len);
   const int key0 = p.prefix + split * p.o_chunk, end = min(key0 + p.o_chunk, n);
   if (k.stats && key0 >= end) return;
   const int i = tile * 16 + l16;
@@ -396,7 +394,7 @@ __global__ __launch_bounds__(256) void join_kernel(Kernel k) {
   if (r >= p.rows) return;
   const int lane = threadIdx.x & 63, sub = lane / kLanes, d = 4 * (lane % kLanes);
   const int b = (int)(r / g.n_q), hq = (int)(r - (size_t)b * g.n_q);
-  const int n = min(max(g.lens[b], 0), g.max_len);
+  const int n = held_length(g.lens[b], g.max_len);
   const int own = n > p.prefix ? (n - p.prefix + p.o_chunk - 1) / p.o_chunk : 0;
   const int live = n > 0 ? p.p_splits + own : 0;
   const float c = g.scale * kLog2e;
@@ -446,9 +444,9 @@ __global__ __launch_bounds__(256) void join_kernel(Kernel k) {
   if (sub == 0) *reinterpret_cast<uint2*>(g.O + r * HEAD + d) = w;
 }
 
-// Two workgroups a CU are one round: chunks are as long as that asks for (512 workgroups), between 128
-// keys (four waves' tiles) and 1,024.
-int chunk_of(long long work) { return (int)std::min(1024LL, std::max(128LL, (work / 512 + 127) / 128 * 128)); }
+// Chunks are as long as 256 workgroups make them, between 128 keys (four waves' tiles) and 1,024: fewer chunks
+// have less to join (9 sequences of up to 1,214 tokens behind 11,136: 21.1 us, with 512 workgroups 22.2).
+int chunk_of(long long work) { return (int)std::min(1024LL, std::max(128LL, (work / 256 + 127) / 128 * 128)); }
 
 DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len) {
   DecodePlan p{};
@@ -457,15 +455,20 @@ DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, in
   p.prefix = B > 1 ? std::min(prefix_len, max_len) : 0;      // (a single sequence shares with nobody)
   const int own = max_len - p.prefix;
   p.o_tiles = (p.group + 15) / 16;
-  if (p.prefix == 0 && own <= 1024) {
+  const long long o_work = (long long)own * B * cache.n_kv * p.o_tiles;
+  // One chunk holds everything: eight waves take it, and there is nothing to join.  (One sequence of 500
+  // tokens, 8 key/value heads: 9.7 us this way, 9.2 in four chunks and a join; of 250: 8.6 and 9.1.)
+  if (p.prefix == 0 && own <= std::max(256, chunk_of(o_work))) {
     p.direct = true;
     p.o_chunk = 1024, p.o_splits = p.splits = 1;
     return p;
   }
-  const long long o_work = (long long)own * B * cache.n_kv * p.o_tiles;
   if (p.prefix > 0) {
     const long long rows = (long long)B * p.group;
-    p.wide = rows > 64;
+    // Sixteen rows at a time read the prefix once per sixteen, from the L2; past 64 MB of that the shared walk is
+    // faster (32 sequences x 4 heads: 1,024 tokens 16.3 us narrow, 17.7 wide; 2,048: 18.7 and 18.4; 4,096: 21.8 and
+    // 20.7; 64 sequences under 8,192: 105 and 71).
+    p.wide = rows > 64 && rows / 16 * p.prefix * cache.n_kv * cache.head * 4 > 64LL << 20;
     p.p_tiles = (int)(p.wide ? (rows + kWideRows - 1) / kWideRows : (rows + 15) / 16);
     const long long p_work = (long long)p.prefix * p.p_tiles * cache.n_kv;
     // wide: a workgroup per CU, or as long a walk as goes along with half the time that the own tokens take to

@@ -50,17 +50,17 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs g) {
   if (g.offsets) {
     b = find_sequence(g.offsets, g.B, t);
     if (b < 0) return;
-    const int first = token_offset(g.offsets, b, g.T);
-    n = token_offset(g.offsets, b + 1, g.T) - first;
+    const int first = held_offset(g.offsets[b], g.T);
+    n = held_count(first, held_offset(g.offsets[b + 1], g.T));
     i = t - first;
   }
-  const long long p = (long long)g.lens[b] - n + i;
-  if (p < 0 || p >= g.positions) return;
+  const int p = held_position(g.lens[b], n, i, g.positions);
+  if (p < 0) return;
   const int page_size = g.cache.page_size, n_kv = g.cache.n_kv, head = g.cache.head;
   const int shift = __builtin_ctz(page_size);
-  const int entry = (int)(p >> shift), slot = (int)p & (page_size - 1);
-  const int page = entry < g.table_width ? g.table[(size_t)b * g.table_width + entry] : -1;
-  const bool kept = page >= 0 && page < g.cache.pages;
+  const int entry = p >> shift, slot = p & (page_size - 1);
+  const int page = entry < g.table_width ? held_page(g.table[(size_t)b * g.table_width + entry], g.cache.pages) : -1;
+  const bool kept = page >= 0;
   const int per = head >> 4, half = head >> 1;             // units of a head, pairs of a head
   const int nq_units = g.n_q * per, nk_units = n_kv * per;
   const float* cs = g.cs + (size_t)p * half;

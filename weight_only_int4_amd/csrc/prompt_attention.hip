@@ -39,8 +39,8 @@ __device__ __forceinline__ bool pick_block(const int32_t* offsets, int B, int T,
                                            int& length) {
   const int lane = threadIdx.x & 63;
   auto range = [&](int b, int& at, int& n) {
-    at = b < B ? token_offset(offsets, b, T) : 0;
-    n = b < B ? max(0, token_offset(offsets, b + 1, T) - at) : 0;
+    at = b < B ? held_offset(offsets[b], T) : 0;
+    n = b < B ? held_count(at, held_offset(offsets[b + 1], T)) : 0;
   };
   auto blocks = [&](int b) {
     int at, n;

@@ -4,6 +4,7 @@
 
 #include <atomic>
 
+#include "held.hpp"
 #include "internal.hpp"
 
 namespace w4 {
@@ -14,11 +15,6 @@ constexpr long long kGridThreads = 0xFFFFFFFFLL;
 // Most elements from one token to the next: 64 tokens stay below 2^32 bytes, the range of a
 // copy's 32-bit offset.
 constexpr long long kMaxStride = 1LL << 24;
-
-// Token offset i of a packed batch, held inside [0, T] whatever the array says.
-__device__ __forceinline__ int token_offset(const int32_t* offsets, int i, int T) {
-  return min(max(offsets[i], 0), T);
-}
 
 // The sequence that token t of a packed batch belongs to, or -1: the last b with
 // offsets[b] <= t, if t < offsets[b + 1].  All 64 lanes of the wave take part, with the same t:
