@@ -494,7 +494,7 @@ int mxfp4_a4_gemm(const uint32_t* Xq, const uint8_t* xscales, int M, int K, int 
  *   bf16 or as w4a8_gemv's int8 activations:
  *     h = bf16(X + residual)  (residual NULL: h = X),   r = 1 / sqrt(mean_k h^2 + eps),
  *     w4_rmsnorm:    Y = bf16((h r) weight), in fp32;
- *     w4a8_rmsnorm:  v = fp32(h weight), t = max_k |v| / 127 (1 where every v is 0),
+ *     w4a8_rmsnorm:  v = fp32(h weight), t = max_k |v| c, c = fp32(1/127) (1 where that is 0),
  *                    Xq = clamp(rint(v / t), -127, 127) (IEEE division, ties to even),
  *                    sx = t r, xsum[m][g] = sum of Xq over the 128 channels of group g.
  *   r multiplies a whole row, so it is left out of the codes and enters the scale: codes

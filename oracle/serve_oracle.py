@@ -31,7 +31,8 @@ def rmsnorm_int8(h, weight, eps):
         v = (h * weight).astype(np.float32)
         top = np.abs(v).max(axis=1)
         bad = ~np.isfinite(v).all(axis=1)
-        t = np.where(top > 0, top / np.float32(127), np.float32(1)).astype(np.float32)
+        t = (top * (np.float32(1) / np.float32(127))).astype(np.float32)
+        t = np.where(t == 0, np.float32(1), t)
         codes = np.clip(np.rint(v / t[:, None]), -127, 127)
         h64 = h.astype(np.float64)
         sx = t.astype(np.float64) / np.sqrt((h64 * h64).mean(axis=1) + eps)

@@ -117,6 +117,22 @@ def test_w4a8_rmsnorm_ties_and_scales():
     assert np.array_equal(int8[0].cpu().numpy(), codes) and np.array_equal(int8[2].cpu().numpy(), xsum)
 
 
+def test_w4a8_rmsnorm_smallest_values():
+    """Products that are subnormal or underflow, and a step that underflows: the codes are the definition's."""
+    rng = np.random.default_rng(18)
+    x = SO.bf16(rng.integers(-255, 256, (6, 256)) * 2.0 ** -133)
+    w = SO.bf16(2.0 ** rng.integers(-20, 1, 256))
+    x[1], x[2] = SO.bf16(np.full(256, 2.0 ** -133)), 0
+    x[3, 1:] = 0
+    w[:8] = 2.0 ** -16
+    *int8, _ = w4.w4a8_rmsnorm(gpu(x), gpu(w), None, 1e-6)
+    _check_norm(x, None, w, 1e-6, None, None, int8)
+    w[:] = 2.0 ** -16                                            # every |v| below 127 of the smallest number
+    *int8, _ = w4.w4a8_rmsnorm(gpu(x[1:4] * 0 + x[1]), gpu(w), None, 1e-6)
+    _check_norm(x[1:4] * 0 + x[1], None, w, 1e-6, None, None, int8)
+    assert not int8[0].any() and (int8[1] > 0).all()
+
+
 @pytest.mark.parametrize("H", [128, 2048, 8192])
 def test_norm_special_rows(H):
     """Zero rows, and rows with infinities and NaN: the latter must not reach their neighbours."""

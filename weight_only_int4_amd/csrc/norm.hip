@@ -1,8 +1,8 @@
 // The residual's addition and the root-mean-square norm, out in bf16 (w4_rmsnorm) or as the
 // int8 activations of the W4A8 linears (w4a8_rmsnorm).
 //   h = bf16(x + residual), r = 1 / sqrt(mean h^2 + eps);  y = bf16((h r) w);
-//   v = fp32(h w), t = max |v| / 127, codes = clamp(rint(v / t)), sx = t r.
-// r > 0 is common to a row's values, so rint(y / (max |y| / 127)) does not depend on it: taking
+//   v = fp32(h w), t = max |v| fp32(1/127), codes = clamp(rint(v / t)), sx = t r.
+// r > 0 is common to a row's values, so rint(127 y / max |y|) does not depend on it: taking
 // the codes from v keeps them exact (v is, both factors having 8-bit significands), while r,
 // whose last bit depends on the order of a sum, enters the scale alone.
 #include "serve.hpp"
@@ -14,6 +14,7 @@ namespace w4 {
 namespace {
 
 constexpr int kNormThreads = 256;
+constexpr float kStep = 1.0f / 127.0f;
 
 __device__ __forceinline__ int row16_sum(int v) {
 #pragma unroll
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const uint16_t* X, c
 #pragma unroll
     for (int i = 0; i < kNormThreads / kWave; ++i) top = max(top, __float_as_uint(red[1][i]));
     const bool finite = top < 0x7F800000u;
-    const float t = top ? __uint_as_float(top) / 127.0f : 1.0f;
+    const float step = __uint_as_float(top) * kStep, t = step > 0.0f ? step : 1.0f;     // (0: of a zero row, or by underflow)
     if (tid == 0) sx[row] = finite ? t * r : __uint_as_float(0x7FC00000u);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
