@@ -149,7 +149,8 @@ struct Flash {
   // Tiles 0 .. tiles - 1 of the workgroup (at least one); this wave takes the first `mine` of them, and
   // calls mask(t), which lays -infinity over scores that are not seen, for those from `masked` on (without
   // MANY: the last one at most).
-  // copy(kv, t, j, lds): copy j of K's (0) or V's (1) tile t.
+  // copy(kv, t, j, lds): copy j of K's (0) or V's (1) tile t; per kv the tiles come in order, the last one
+  // several times.
   // One barrier a tile, between its weights and its products (values of the tile, scores of the next):
   // behind it nobody reads K of tile t or V of tile t - 1 any more; the copies of K of tile t + 2 and V of
   // tile t + 1 are issued among the products and have to be there at the next.
@@ -200,12 +201,7 @@ struct Flash {
     if (mine > 0) {
       products(no, yes, 0);
       const int hot = MANY ? min(mine - 1, masked) : mine - 1;
-      if (hot > 0) raise();
-      // Tiles without masks.  The reference is the first tile's maximum and stays while the p of a row sum to
-      // less than 2^30: fp32 and bf16 lose nothing by that, and neither the maximum has to be found nor the
-      // accumulators to be scaled.  (Values so large that it overflows come out infinite, and the callers
-      // take such rows up again.)
-      while (t < hot) {
+      auto weigh = [&]() {
         float sum = weights();
         if (__ballot(!(sum < 0x1p30f))) {
           asm volatile("");                   // a branch, not both ways and a choice
@@ -213,6 +209,14 @@ struct Flash {
           sum = weights();
         }
         lsum += sum;
+      };
+      if (hot > 0) raise();
+      // Tiles without masks.  The reference is the first tile's maximum and stays while the p of a row sum to
+      // less than 2^30: fp32 and bf16 lose nothing by that, and neither the maximum has to be found nor the
+      // accumulators to be scaled.  (Values so large that it overflows come out infinite, and the callers
+      // take such rows up again.)
+      while (t < hot) {
+        weigh();
         turn();
         products(yes, yes, (t & 1) ^ 1);
         ++t;
@@ -227,8 +231,8 @@ struct Flash {
         }
       }
       if (t >= masked) mask(t);
-      raise();
-      lsum += weights();
+      if (t == 0 || MANY) raise();
+      weigh();
       turn();
       products(yes, no, 0);
       ++t;

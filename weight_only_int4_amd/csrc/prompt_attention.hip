@@ -117,14 +117,20 @@ __global__ __launch_bounds__(WAVES * 64, 2) void prompt_kernel(PromptArgs g, int
     koff[0][j] = r * kstep + F::k_piece(), koff[1][j] = q * kstep + F::k_piece();
     voff[0][j] = r * vstep + F::v_piece(), voff[1][j] = q * vstep + F::v_piece();
   }
+  // tiles come in order: their addresses are steps from one to the next
+  const size_t kpitch = (size_t)kTile * g.k_stride, vpitch = (size_t)kTile * g.v_stride;
+  int kt = 0, vt = 0;
   f.template walk<false>(
       tiles, my_tiles, my_tiles - 1,
       [&](int kv, int t, int j, uint32_t lds) {
-        const int whole = t < cut ? 0 : 1;
-        if (kv == 0)
-          lds_copy16_free(whole ? koff[1][j] : koff[0][j], kbase + (size_t)(t * kTile) * g.k_stride, lds);
-        else
-          lds_copy16_free(whole ? voff[1][j] : voff[0][j], vbase + (size_t)(t * kTile) * g.v_stride, lds);
+        const bool rest = t >= cut;
+        if (kv == 0) {
+          kbase += t > kt ? kpitch : 0, kt = t;
+          lds_copy16_free(rest ? koff[1][j] : koff[0][j], kbase, lds);
+        } else {
+          vbase += t > vt ? vpitch : 0, vt = t;
+          lds_copy16_free(rest ? voff[1][j] : voff[0][j], vbase, lds);
+        }
       },
       [&](int t) {                            // the diagonal, or the sequence's end
         const int end = min(q0 + l32, n - 1) - t * kTile - 4 * h;
@@ -164,8 +170,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void prompt_kernel(PromptArgs g, int
     todo &= todo - 1;
     attend<HEAD>(g.Q + (size_t)(first + i) * g.q_stride + (size_t)hq * HEAD, i + 1, g.scale,
                  [&](int key, const uint16_t*& k, const uint16_t*& v) {
-                   k = kbase + (size_t)key * g.k_stride;
-                   v = vbase + (size_t)key * g.v_stride;
+                   k = g.K + (size_t)(first + key) * g.k_stride + (size_t)kvh * HEAD;
+                   v = g.V + (size_t)(first + key) * g.v_stride + (size_t)kvh * HEAD;
                  },
                  g.O + ((size_t)(first + i) * g.n_q + hq) * HEAD);
   }
