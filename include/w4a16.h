@@ -572,7 +572,7 @@ int w4_prompt_attention(const uint16_t* Q, long long q_stride, const uint16_t* K
  *   Q [B][n_q][head] with its stride.  lens [B] int32 device; a sequence of length 0 gets zeros, one
  *   shorter than the prefix sees its first lens[b] tokens.  max_len: no sequence is longer
  *   (tokens from max_len on are left out); the work is laid out by it, lengths may change
- *   between replays of a graph.  max_len and prefix_len at most table_width page_size.
+ *   between replays of a graph.  max_len and prefix_len at most table_width page_size and 2^30.
  *   O [B][n_q][head] bf16 out.
  *   Size query and workspace as in w4a16_gemv; the size depends only on B, n_q, max_len,
  *   prefix_len and the cache's page_size, n_kv and head (its pointers may be NULL then).

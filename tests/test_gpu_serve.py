@@ -230,7 +230,7 @@ def _run_append(case, use_offsets=True, with_k=True):
 
 
 @pytest.mark.parametrize("n_q,n_kv,head,page", [(16, 8, 128, 16), (4, 1, 64, 256), (5, 5, 64, 32), (7, 1, 128, 64), (24, 2, 128, 128)])
-@pytest.mark.parametrize("new,before", [([1], [0]), ([37, 1, 0, 64, 5], [0, 90, 3, 16, 255]), ([0, 0, 200, 0], [5, 0, 1, 0]), ([3] * 70, [11] * 70)])
+@pytest.mark.parametrize("new,before", [([1], [0]), ([37, 1, 0, 64, 5], [0, 90, 3, 16, 255]), ([0, 0, 200, 0], [5, 0, 1, 0]), ([3] * 70, [11] * 70), ([1, 0] * 2500, [3, 7] * 2500)])
 def test_append(n_q, n_kv, head, page, new, before):
     say("append", n_q, n_kv, head, page, new[:5])
     _run_append(_append_case(np.random.default_rng(len(new) + head), new, before, n_q, n_kv, head, page))
@@ -408,6 +408,56 @@ def test_prompt_attention_long(head, n_q, n_kv, lengths):
     check_prompt(o, q, k, v, lengths, head ** -0.5, heads=range(min(n_q, 3)))
 
 
+@pytest.mark.parametrize("head,n_q,n_kv,lengths", [(128, 16, 8, [8300]), (64, 16, 2, [5000, 3300, 1]), (128, 24, 3, [65, 5000, 0, 900]), (64, 17, 17, [7800])])
+def test_prompt_attention_many_rows(head, n_q, n_kv, lengths):
+    """Past the row count from which eight waves share key tiles: rows at both ends and between, of some heads."""
+    say("prompt many rows", head, n_q, n_kv, lengths)
+    T = sum(lengths)
+    assert T * n_q >= 512 * 256
+    q, k, v = fused(generator(T), T, n_q, n_kv, head)
+    o = w4.prompt_attention(q, k, v, ints(offsets_of(lengths)))
+    assert same_bits(o, w4.prompt_attention(q, k, v, ints(offsets_of(lengths))))
+    go, gq, gk, gv = (t.double().cpu() for t in (o, q, k, v))
+    c, at, group = Checker(head), 0, n_q // n_kv
+    for n in lengths:
+        for h in (0, n_q // 2, n_q - 1):
+            for first in sorted({0, max(0, n // 2 - 77), max(0, n - 130)}):
+                rows = min(130, n - first)
+                if rows <= 0:
+                    continue
+                seen = torch.arange(first + rows)[None, :] <= torch.arange(first, first + rows)[:, None]
+                c.add(go[at + first:at + first + rows, h], gq[at + first:at + first + rows, h], gk[at:at + first + rows, h // group],
+                      gv[at:at + first + rows, h // group], head ** -0.5, seen)
+        at += n
+    c.done()
+
+
+@pytest.mark.parametrize("lengths", [[3] * 300, [1] * 5000, [0, 2] * 200 + [700] + [5] * 100, [1 + i % 90 for i in range(257)]])
+def test_prompt_attention_many_sequences(lengths):
+    say("prompt many sequences", len(lengths))
+    T = sum(lengths)
+    q, k, v = fused(generator(len(lengths)), T + 3, 4, 2, 64)
+    o = torch.full((T + 3, 4, 64), 7.0, dtype=BF, device="cuda")
+    w4.prompt_attention(q, k, v, ints(offsets_of(lengths)), O=o)
+    assert (o[T:] == 7).all()
+    check_prompt(o[:T], q[:T], k[:T], v[:T], lengths, 64 ** -0.5, heads=(0, 3))
+
+
+def test_packed_rows_before_the_first_sequence():
+    """offsets[0] > 0: the rows before it belong to no sequence."""
+    q, k, v = fused(generator(31), 200, 4, 2, 128)
+    k[:50], v[:50] = NAN, NAN
+    o = torch.full((200, 4, 128), 7.0, dtype=BF, device="cuda")
+    w4.prompt_attention(q, k, v, ints([50, 120, 190]), O=o)
+    assert (o[:50] == 7).all() and (o[190:] == 7).all()
+    check_prompt(o[50:190], q[50:190], k[50:190], v[50:190], [70, 70], 128 ** -0.5)
+    cs, sn = w4.rope_table(100)
+    qo = torch.full((200, 4, 128), 7.0, dtype=BF, device="cuda")
+    kc = torch.zeros(8, 2, 64, 128, dtype=BF, device="cuda")
+    w4.kv_append(q, k, v, cs, sn, kc, torch.zeros_like(kc), ints([70, 70]), ints([[0, 1], [2, 3]]), ints([50, 120, 190]), Q_out=qo)
+    assert (qo[:50] == 7).all() and (qo[190:] == 7).all() and not (qo[50:190] == 7).all(dim=2).any() and not kc[4:].any()
+
+
 @pytest.mark.parametrize("head", [64, 128])
 def test_prompt_attention_scales(head):
     """Sharp and flat softmax; scores in the thousands neither overflow nor lose the maximum."""
@@ -521,7 +571,7 @@ def check_decode(got, q, keys, values, scale):
 
 
 DECODE = [([1], 0), ([500], 0), ([0, 1, 15, 16, 17, 0, 33, 300], 0), ([257] * 3, 256), ([300, 256, 800, 257, 512], 256), ([2100, 2049], 2048),
-          ([1025 + 7 * i for i in range(20)], 1024), ([5, 300, 0, 256, 100, 700], 256), ([4000, 1, 2], 0), ([513] * 70, 512), ([40] * 65, 0)]
+          ([1025 + 7 * i for i in range(20)], 1024), ([5, 300, 0, 256, 100, 700], 256), ([4000, 1, 2], 0), ([513] * 70, 512), ([40] * 65, 0), ([260] * 300 + [0] * 10 + [257], 256)]
 
 
 @pytest.mark.parametrize("head", [64, 128])

@@ -226,7 +226,9 @@ def test_decode_refusals(lib):
     assert lib.w4_decode_attention(A, 256, 3, 4, None, A, A, 5, 80, 32, 0.1, A, None, None, None) == -1
     assert _decode(lib, _cache(head=32)) == -4 and _decode(lib, _cache(page_size=17)) == -4
     for kw in (dict(B=-1), dict(n_q=3), dict(max_len=-1), dict(max_len=81), dict(prefix=-16), dict(prefix=24), dict(prefix=96),
-               dict(width=-1), dict(qs=128), dict(qs=260)):
+               dict(width=-1), dict(qs=128), dict(qs=260), dict(width=2 ** 31 - 1, max_len=2 ** 31 - 1),
+               dict(width=2 ** 31 - 1, max_len=2 ** 30 + 1), dict(B=2 ** 31 - 1), dict(B=2 ** 23, width=2 ** 20, max_len=2 ** 23),
+               dict(width=2 ** 27, max_len=2 ** 30, prefix=2 ** 30 + 16)):
         assert _decode(lib, **kw) == -2, kw
     for scale in (0.0, -1.0, math.nan, math.inf):
         assert _decode(lib, scale=scale) == -7
@@ -235,6 +237,28 @@ def test_decode_refusals(lib):
         assert _decode(lib, **{name: MIS}) == -3, name
     assert _decode(lib, _cache(v=None)) == -1 and _decode(lib, _cache(k=0x10008)) == -3
     assert _decode(lib, B=0, Q=None) == 0
+
+
+def test_decode_workspace_sizes(lib):
+    """The size query over the range of its arguments: monotonous plans, no wrap-around, and the same for the same call."""
+    def size(B, n_q, max_len, prefix, **kw):
+        c, out = _cache(**kw), ctypes.c_size_t(0)
+        rc = lib.w4_decode_attention(None, 0, B, n_q, ctypes.byref(c), None, None, 0, max_len, prefix, 0.0, None, None, ctypes.byref(out), None)
+        return rc, out.value
+    assert size(1, 4, 100, 0) == (0, 0) and size(0, 4, 100, 32) == (0, 0)
+    for B in (1, 2, 3, 16, 64, 65, 200, 1000):
+        for max_len in (0, 1, 127, 500, 1025, 5000, 70000):
+            for prefix in (0, 16, 512, 4096):
+                for heads in ((1, 1), (16, 8), (64, 4), (48, 1)):
+                    rc, n = size(B, heads[0], max_len, prefix, n_kv=heads[1], head=128)
+                    rows = B * heads[0]
+                    assert rc == 0 and n == size(B, heads[0], max_len, prefix, n_kv=heads[1], head=128)[1]
+                    # splits x rows x (m, l and 128 sums), the first part rounded up to 256 bytes
+                    assert n == 0 or any(n == -(-k * rows * 8 // 256) * 256 + k * rows * 512 for k in range(1, 2000))
+                    if B > 1 and prefix and max_len:
+                        assert n > 0
+    rc, n = size(1, 1, 2 ** 30, 0, n_kv=1)
+    assert rc == 0 and n >= 2 ** 20 * (8 + 4 * 64)
 
 
 def test_binding_refusals():

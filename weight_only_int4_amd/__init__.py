@@ -980,7 +980,7 @@ def _decode_attention(Q, k_cache, v_cache, lens, table, max_len, prefix_len, sca
     n_q, q_stride = _heads(Q, "Q", B, head, dev)
     width = _table_width(table, B, dev)
     if max_len is None:
-        max_len = min(width * cache.page_size, 2 ** 31 - 1)
+        max_len = min(width * cache.page_size, 2 ** 30)
     if not 0 <= max_len < 2 ** 31 or not 0 <= prefix_len < 2 ** 31:
         raise ValueError("max_len and prefix_len must be whole numbers of tokens below 2^31")
     if O is None:

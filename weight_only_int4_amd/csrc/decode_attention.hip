@@ -468,12 +468,12 @@ DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, in
     // Sixteen rows at a time read the prefix once per sixteen, from the L2; past 64 MB of that the shared walk is
     // faster (32 sequences x 4 heads: 1,024 tokens 16.3 us narrow, 17.7 wide; 2,048: 18.7 and 18.4; 4,096: 21.8 and
     // 20.7; 64 sequences under 8,192: 105 and 71).
-    p.wide = rows > 64 && rows / 16 * p.prefix * cache.n_kv * cache.head * 4 > 64LL << 20;
+    p.wide = rows > 64 && (double)rows / 16 * p.prefix * cache.n_kv * cache.head * 4 > 64 << 20;
     p.p_tiles = (int)(p.wide ? (rows + kWideRows - 1) / kWideRows : (rows + 15) / 16);
     const long long p_work = (long long)p.prefix * p.p_tiles * cache.n_kv;
     // wide: a workgroup per CU, or as long a walk as goes along with half the time that the own tokens take to
     // read (a tile of 64 keys takes 1.3 us, a CU's share of the memory's rate is about 18 GB/s)
-    const long long along = o_work / p.o_tiles * cache.head / 45000;
+    const long long along = (long long)std::min(1024.0, (double)o_work / p.o_tiles * cache.head / 45000);
     p.p_chunk = p.wide ? (int)std::min(1024LL, std::max(256LL, (std::max(p_work / 256, along) + 63) / 64 * 64))
                        : chunk_of(p_work + o_work);
     p.o_chunk = p.wide ? chunk_of(o_work) : p.p_chunk;
@@ -498,7 +498,11 @@ size_t decode_workspace_bytes(int B, int n_q, const w4_kv_cache& cache, int max_
   return B == 0 ? 0 : plan_decode(B, n_q, cache, max_len, prefix_len).bytes;
 }
 
+// Rows below 2^31 and lengths to 2^30 keep the plan's numbers within 64 bits and a chunk's last key within an int;
+// the grid's limit then keeps splits x rows below 2^31.
+
 bool decode_fits(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len) {
+  if ((long long)B * n_q > 0x7FFFFFFFLL || max_len > 1 << 30 || prefix_len > 1 << 30) return false;
   const DecodePlan p = plan_decode(B, n_q, cache, max_len, prefix_len);
   return chunk_blocks(p, B, cache.n_kv) * 512 <= kGridThreads && (long long)((p.rows + 3) / 4) * 256 <= kGridThreads;
 }

@@ -47,13 +47,17 @@ __device__ __forceinline__ bool pick_block(const int32_t* offsets, int B, int T,
     range(b, at, n);
     return (n + size - 1) / size;
   };
-  int at, n;
-  range(lane, at, n);
-  const int mine = (n + size - 1) / size;     // of the first 64 sequences: held
+  constexpr int kHeld = 4;                    // blocks of the first 256 sequences: held
+  int mine[kHeld], at, n;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) mine[i] = 64 * i < B ? blocks(64 * i + lane) : 0;
   auto from = [&](int j) {                    // blocks of index j and more
-    int n = max(0, mine - j);
-    for (int b = 64; b < B; b += 64) n += max(0, blocks(b + lane) - j);
-    return wave_sum_int(n);
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) sum += max(0, mine[i] - j);
+#pragma unroll 4
+    for (int b = 64 * kHeld; b < B; b += 64) sum += max(0, blocks(b + lane) - j);
+    return wave_sum_int(sum);
   };
   const int total = from(0);
   if (total <= rank) return false;
@@ -67,7 +71,7 @@ __device__ __forceinline__ bool pick_block(const int32_t* offsets, int B, int T,
   block = lo;
   int k = rank - above;                       // the k-th sequence with more than lo blocks
   for (int b = 0; b < B; b += 64) {
-    if (b) range(b + lane, at, n);
+    range(b + lane, at, n);
     unsigned long long set = __ballot((n + size - 1) / size > lo);
     const int count = __popcll(set);
     if (k < count) {
