@@ -13,7 +13,7 @@ namespace w4 {
 
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kMostThreads = 1024;
 constexpr float kStep = 1.0f / 127.0f;
 
 __device__ __forceinline__ int row16_sum(int v) {
@@ -22,20 +22,20 @@ __device__ __forceinline__ int row16_sum(int v) {
   return v;
 }
 
-// One workgroup per row; thread i holds the 8-channel chunks i, i + 256, ... of h, so the row is
-// read once.
+// One workgroup per row of as many waves as CH chunks of 8 channels a thread leave work for (H = 5,120: five
+// waves, two chunks), so that the row is read once, held, and no lane idles.
 template <int CH, bool INT8>
-__global__ __launch_bounds__(kNormThreads) void norm_kernel(const uint16_t* X, const uint16_t* R, int H,
+__global__ __launch_bounds__(kMostThreads) void norm_kernel(const uint16_t* X, const uint16_t* R, int H,
                                                             const uint16_t* __restrict__ w, float eps, uint16_t* hout,
                                                             uint16_t* Y, int8_t* Xq, float* sx, int32_t* xsum) {
-  __shared__ float red[2][kNormThreads / kWave];
+  __shared__ float red[2][kMostThreads / kWave];
   const size_t row = blockIdx.x;
-  const int tid = threadIdx.x, chunks = H >> 3;
+  const int tid = threadIdx.x, threads = blockDim.x, waves = threads >> 6, chunks = H >> 3;
   uint4 hv[CH];
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = tid + i * kNormThreads;
+    const int c = tid + i * threads;
     hv[i] = make_uint4(0u, 0u, 0u, 0u);
     if (c >= chunks) continue;
     hv[i] = *reinterpret_cast<const uint4*>(X + row * H + 8 * c);
@@ -62,13 +62,12 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const uint16_t* X, c
   if ((tid & 63) == 0) red[0][tid >> 6] = ss;
   __syncthreads();
   ss = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kNormThreads / kWave; ++i) ss = ss + red[0][i];
+  for (int i = 0; i < waves; ++i) ss = ss + red[0][i];
   const float r = 1.0f / sqrtf(ss / (float)H + eps);
   if constexpr (!INT8) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = tid + i * kNormThreads;
+      const int c = tid + i * threads;
       if (c >= chunks) continue;
       const uint4 wv = *reinterpret_cast<const uint4*>(w + 8 * c);
       const uint32_t d[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w}, e[4] = {wv.x, wv.y, wv.z, wv.w};
@@ -86,7 +85,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const uint16_t* X, c
     uint32_t top = 0u;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = tid + i * kNormThreads;
+      const int c = tid + i * threads;
       if (c >= chunks) continue;
       const uint4 wv = *reinterpret_cast<const uint4*>(w + 8 * c);
       const uint32_t d[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w}, e[4] = {wv.x, wv.y, wv.z, wv.w};
@@ -102,14 +101,13 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const uint16_t* X, c
     if ((tid & 63) == 0) red[1][tid >> 6] = __uint_as_float(top);
     __syncthreads();
     top = 0u;
-#pragma unroll
-    for (int i = 0; i < kNormThreads / kWave; ++i) top = max(top, __float_as_uint(red[1][i]));
+    for (int i = 0; i < waves; ++i) top = max(top, __float_as_uint(red[1][i]));
     const bool finite = top < 0x7F800000u;
     const float step = __uint_as_float(top) * kStep, t = step > 0.0f ? step : 1.0f;     // (0: of a zero row, or by underflow)
     if (tid == 0) sx[row] = finite ? t * r : __uint_as_float(0x7FC00000u);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = tid + i * kNormThreads;
+      const int c = tid + i * threads;
       int part = 0;
       if (c < chunks) {
         const uint4 wv = *reinterpret_cast<const uint4*>(w + 8 * c);
@@ -134,26 +132,28 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const uint16_t* X, c
 
 template <int CH>
 void launch(const NormArgs& a, hipStream_t st) {
+  const int threads = ((a.H / 8 + CH - 1) / CH + kWave - 1) / kWave * kWave;
   if (a.Xq)
-    hipLaunchKernelGGL((norm_kernel<CH, true>), dim3(a.T), dim3(kNormThreads), 0, st, a.X, a.residual, a.H, a.weight,
-                       a.eps, a.h, a.Y, a.Xq, a.sx, a.xsum);
+    hipLaunchKernelGGL((norm_kernel<CH, true>), dim3(a.T), dim3(threads), 0, st, a.X, a.residual, a.H, a.weight, a.eps,
+                       a.h, a.Y, a.Xq, a.sx, a.xsum);
   else
-    hipLaunchKernelGGL((norm_kernel<CH, false>), dim3(a.T), dim3(kNormThreads), 0, st, a.X, a.residual, a.H, a.weight,
-                       a.eps, a.h, a.Y, a.Xq, a.sx, a.xsum);
+    hipLaunchKernelGGL((norm_kernel<CH, false>), dim3(a.T), dim3(threads), 0, st, a.X, a.residual, a.H, a.weight, a.eps,
+                       a.h, a.Y, a.Xq, a.sx, a.xsum);
 }
 
 }  // namespace
 
-bool norm_fits(int T) { return (long long)T * kNormThreads <= kGridThreads; }
+bool norm_fits(int T) { return (long long)T * kMostThreads <= kGridThreads; }
 
 int launch_norm(const NormArgs& a, hipStream_t st) {
-  const int per = (a.H / 8 + kNormThreads - 1) / kNormThreads;
-  if (per <= 1) launch<1>(a, st);
-  else if (per <= 2) launch<2>(a, st);
-  else if (per <= 4) launch<4>(a, st);
-  else if (per <= 8) launch<8>(a, st);
-  else if (per <= 16) launch<16>(a, st);
-  else launch<32>(a, st);
+  // Few rows: as many threads as there are chunks, up to 1,024 (1 x 5,120: 4.1 us with 256 threads, 3.2; int8,
+  // 16 x 17,408: 14.8 and 8.4).  Many: two chunks a thread (int8, 8,191 x 5,120: 78 us with one, 71 with two, 75
+  // with five, 82 with ten and one wave a row; 4,096 x 2,048: 13.3 with one, 12.5 with two).
+  const int chunks = a.H / 8;
+  if (chunks <= 1024 && a.T <= 512) launch<1>(a, st);
+  else if (chunks <= 2048) launch<2>(a, st);
+  else if (chunks <= 4096) launch<4>(a, st);
+  else launch<8>(a, st);
   W4_CHECK_LAUNCH();
   return W4_OK;
 }
