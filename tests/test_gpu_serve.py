@@ -117,6 +117,17 @@ def test_w4a8_rmsnorm_ties_and_scales():
     assert np.array_equal(int8[0].cpu().numpy(), codes) and np.array_equal(int8[2].cpu().numpy(), xsum)
 
 
+def test_w4a8_rmsnorm_quotients_next_to_halves():
+    """Two million quotients of steps that are no powers of two: some hundred of them lie within 2^-14 of a half, where
+    a product with the step's reciprocal could round the other way."""
+    rng = np.random.default_rng(81)
+    x = normal(rng, 2048, 1024) * np.float32(2.0) ** rng.integers(-90, 90, (2048, 1)).astype(np.float32)
+    x, w = SO.bf16(x), SO.bf16(1 + 0.5 * rng.standard_normal(1024))
+    codes, _, xsum = SO.rmsnorm_int8(x, w, 0.0)
+    *int8, _ = w4.w4a8_rmsnorm(gpu(x), gpu(w), None, 0.0)
+    assert np.array_equal(int8[0].cpu().numpy(), codes) and np.array_equal(int8[2].cpu().numpy(), xsum)
+
+
 def test_w4a8_rmsnorm_smallest_values():
     """Products that are subnormal or underflow, and a step that underflows: the codes are the definition's."""
     rng = np.random.default_rng(18)

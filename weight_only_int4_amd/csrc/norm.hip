@@ -5,6 +5,10 @@
 // r > 0 is common to a row's values, so rint(127 y / max |y|) does not depend on it: taking
 // the codes from v keeps them exact (v is, both factors having 8-bit significands), while r,
 // whose last bit depends on the order of a sum, enters the scale alone.
+//
+// What bounds it: a few rows the launch (int8, 1 x 2,048: 3.1 us in the kernel, a round trip to memory and two
+// barriers); many rows the memory (int8, 8,191 x 5,120 with a residual: 294 MB in 70 us, 4.2 TB/s; 4,096 x 2,048 in
+// bf16: 67 MB in 12.1 us, part of it from the caches).
 #include "serve.hpp"
 
 #pragma clang fp contract(off)
@@ -104,6 +108,10 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(const uint16_t* X, c
     for (int i = 0; i < waves; ++i) top = max(top, __float_as_uint(red[1][i]));
     const bool finite = top < 0x7F800000u;
     const float step = __uint_as_float(top) * kStep, t = step > 0.0f ? step : 1.0f;     // (0: of a zero row, or by underflow)
+    // Eight divisions a chunk are 75 us at 8,191 x 5,120, eight products 70.  v / t by the reciprocal is off by less than 2^-15 (values to 127, three roundings of 2^-24), so where it lies
+    // 2^-14 or more from a half it rounds as the quotient does; the others, and steps so small that the reciprocal
+    // might overflow, are divided.
+    const float inv = 1.0f / t, far = t >= 0x1p-100f ? 1.0f : 0.0f;
     if (tid == 0) sx[row] = finite ? t * r : __uint_as_float(0x7FC00000u);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -112,15 +120,27 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(const uint16_t* X, c
       if (c < chunks) {
         const uint4 wv = *reinterpret_cast<const uint4*>(w + 8 * c);
         const uint32_t d[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w}, e[4] = {wv.x, wv.y, wv.z, wv.w};
-        uint32_t packed[2] = {0u, 0u};
+        float v[8], q[8], near = far;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint32_t a = (j & 1) ? (d[j >> 1] & 0xFFFF0000u) : (d[j >> 1] << 16);
-          const uint32_t b = (j & 1) ? (e[j >> 1] & 0xFFFF0000u) : (e[j >> 1] << 16);
-          const float q = __builtin_rintf((__uint_as_float(a) * __uint_as_float(b)) / t);
-          const int code = finite ? (int)fminf(fmaxf(q, -127.0f), 127.0f) : 0;
-          part += code;
-          packed[j >> 2] |= ((uint32_t)code & 0xFFu) << (8 * (j & 3));
+          const uint32_t x = (j & 1) ? (d[j >> 1] & 0xFFFF0000u) : (d[j >> 1] << 16);
+          const uint32_t y = (j & 1) ? (e[j >> 1] & 0xFFFF0000u) : (e[j >> 1] << 16);
+          v[j] = __uint_as_float(x) * __uint_as_float(y);
+          const float z = v[j] * inv;
+          q[j] = __builtin_rintf(z);
+          near = fminf(near, 0.5f - fabsf(z - q[j]));
+        }
+        if (!(near > 0x1p-14f)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) q[j] = fminf(fmaxf(__builtin_rintf(v[j] / t), -127.0f), 127.0f);
+        }
+        uint32_t packed[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t lo = __builtin_amdgcn_perm((uint32_t)(int)q[4 * w + 1], (uint32_t)(int)q[4 * w], 0x0C0C0400u);
+          const uint32_t hi = __builtin_amdgcn_perm((uint32_t)(int)q[4 * w + 3], (uint32_t)(int)q[4 * w + 2], 0x04000C0Cu);
+          packed[w] = finite ? lo | hi : 0u;
+          part = __builtin_amdgcn_sdot4((int)packed[w], 0x01010101, part, false);
         }
         *reinterpret_cast<uint2*>(Xq + row * H + 8 * c) = make_uint2(packed[0], packed[1]);
       }
@@ -147,8 +167,8 @@ bool norm_fits(int T) { return (long long)T * kMostThreads <= kGridThreads; }
 
 int launch_norm(const NormArgs& a, hipStream_t st) {
   // Few rows: as many threads as there are chunks, up to 1,024 (1 x 5,120: 4.1 us with 256 threads, 3.2; int8,
-  // 16 x 17,408: 14.8 and 8.4).  Many: two chunks a thread (int8, 8,191 x 5,120: 78 us with one, 71 with two, 75
-  // with five, 82 with ten and one wave a row; 4,096 x 2,048: 13.3 with one, 12.5 with two).
+  // 16 x 17,408: 14.8 and 8.4).  Many: two chunks a thread (int8 with divisions, 8,191 x 5,120: 78 us with one, 71
+  // with two, 75 with five, 82 with ten and one wave a row; 4,096 x 2,048: 13.3 with one, 12.5 with two).
   const int chunks = a.H / 8;
   if (chunks <= 1024 && a.T <= 512) launch<1>(a, st);
   else if (chunks <= 2048) launch<2>(a, st);
