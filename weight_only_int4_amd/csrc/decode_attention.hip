@@ -5,6 +5,10 @@
 // own.  Every chunk gives, per row, the largest score m, the sum l of p = exp(scale (s - m)) and sum p V in
 // fp32; a second kernel joins a row's chunks: O = sum_c w_c O_c / sum_c w_c l_c, w_c = exp(scale (m_c - max m)).
 // Chunk sizes follow from what the host knows, so a captured graph serves any lengths.
+//
+// What bounds it: long lengths the memory (64 sequences of 2,000 tokens behind 8,192, 32 heads on 8: 302 MB from
+// it and 66 us in the chunks, 4.6 TB/s); short ones the way of one chunk from the lengths over the table, keys,
+// scores and values to LDS and out, 5 us, and a second launch of 4 (16 sequences of 512 behind 2,048: 9.6 and 4.5).
 #include "attend.hpp"
 #include "flash_tile.hpp"
 
@@ -457,8 +461,8 @@ DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, in
   p.o_tiles = (p.group + 15) / 16;
   const long long o_work = (long long)own * B * cache.n_kv * p.o_tiles;
   // One chunk holds everything: eight waves take it, and there is nothing to join.  (One sequence of 500
-  // tokens, 8 key/value heads: 9.7 us this way, 9.2 in four chunks and a join; of 250: 8.6 and 9.1.)
-  if (p.prefix == 0 && own <= std::max(256, chunk_of(o_work))) {
+  // tokens, 8 key/value heads: 9.9 us this way, 9.3 in four chunks and a join; of 380: 8.8 and 9.3; 250: 7.7 and 9.2.)
+  if (p.prefix == 0 && own <= std::max(384, chunk_of(o_work))) {
     p.direct = true;
     p.o_chunk = 1024, p.o_splits = p.splits = 1;
     return p;
@@ -471,8 +475,9 @@ DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, in
     p.wide = rows > 64 && (double)rows / 16 * p.prefix * cache.n_kv * cache.head * 4 > 64 << 20;
     p.p_tiles = (int)(p.wide ? (rows + kWideRows - 1) / kWideRows : (rows + 15) / 16);
     const long long p_work = (long long)p.prefix * p.p_tiles * cache.n_kv;
-    // wide: a workgroup per CU, or as long a walk as goes along with half the time that the own tokens take to
-    // read (a tile of 64 keys takes 1.3 us, a CU's share of the memory's rate is about 18 GB/s)
+    // wide: a workgroup per CU, or longer walks on fewer of them while the own tokens are many enough to be read
+    // beside them (64 sequences of 2,000 tokens behind 8,192: 70.5 us, with a workgroup per CU 78.8; of 1,000: 50.2
+    // and 56.7; twice or half the divisor changes nothing)
     const long long along = (long long)std::min(1024.0, (double)o_work / p.o_tiles * cache.head / 45000);
     p.p_chunk = p.wide ? (int)std::min(1024LL, std::max(256LL, (std::max(p_work / 256, along) + 63) / 64 * 64))
                        : chunk_of(p_work + o_work);
