@@ -9,11 +9,13 @@
 //
 // What bounds it: per tile and wave 32 matrix instructions of 32 cycles (head 128; 16 for head 64) and
 // about 100 vector instructions of 4, of which 32 exp2 take 8, and every matrix instruction holds the vector
-// ALU up for about 9; on random data the chip also lowers its clock (1 x 8192 tokens of 16 heads: a fifth
-// faster on zeros).  Two waves a SIMD overlap the one with the other.  Measured and not kept: the weights
-// of tile t + 1 woven between the matrix instructions of tile t in one wave (no change at head 128, where
-// another 50 registers are no loss; 97 -> 119 us for 12 x 2047 ragged at head 64, where they cost waves), the two
-// waves of a SIMD in opposite phases by a second barrier (no change), tiles of 128 keys at head 64 (97 -> 110).
+// ALU up for about 9; on random data the chip also lowers its clock (1 x 8192 tokens of 16 heads of 128: 251 us,
+// 1.1 PFLOP/s of the 1.42 that a large matrix product reaches; on zeros 204.  12 x 2047 ragged at head 64: 96).
+// Two waves a SIMD overlap the one with the other.  Measured and not kept: the weights of tile t + 1 woven between
+// the matrix instructions of tile t in one wave (no change at head 128, where another 50 registers are no loss;
+// 97 -> 119 us at head 64, where they cost waves), the two waves of a SIMD in opposite phases by a second barrier
+// or by s_setprio (no change), 64 queries a wave with all 512 registers (1 x 8192: 395 us), tiles of 128 keys at
+// head 64 (97 -> 110), a barrier every two tiles (267 -> 269 and 100 -> 104).
 #pragma once
 
 #include <math.h>
@@ -128,7 +130,8 @@ struct Flash {
     mc = m == -INFINITY ? 0.0f : -m * c;
   }
 
-  // The weights of a tile and their sum: of the rounded p, as the product with V has them.
+  // The weights of a tile and their sum: of the rounded p, as the product with V has them.  (The dot products
+  // keep the matrix unit for a while; additions in their place: 95 -> 116 us at head 64, no change at 128.)
   __device__ __forceinline__ float weights() {
     const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
     float sum[2] = {0.0f, 0.0f};
