@@ -7,8 +7,8 @@
 // whose last bit depends on the order of a sum, enters the scale alone.
 //
 // What bounds it: a few rows the launch (int8, 1 x 2,048: 3.1 us in the kernel, a round trip to memory and two
-// barriers); many rows the memory (int8, 8,191 x 5,120 with a residual: 294 MB in 70 us, 4.2 TB/s; 4,096 x 2,048 in
-// bf16: 67 MB in 12.1 us, part of it from the caches).
+// barriers); many rows the memory (int8, 8,191 x 5,120 with a residual: 294 MB in 65 to 70 us, 4.5 to 4.2 TB/s; 4,096 x
+// 2,048 in bf16: 67 MB in 11.5 to 12.1 us, part of it from the caches).
 #include "serve.hpp"
 
 #pragma clang fp contract(off)
