@@ -664,6 +664,48 @@ def test_decode_attention_short_rows_under_a_prefix_with_nan():
     assert torch.isnan(o[0, :2].float()).all() and torch.isnan(o[0, 2:, 7].float()).all()
 
 
+@pytest.mark.parametrize("lens,prefix,first,end", [
+    ([33], 0, 32, 33), ([300], 0, 288, 300), ([641], 0, 640, 641), ([600, 33, 900], 0, 32, 33), ([300] * 3, 256, 32, 64),
+    ([700] * 40, 512, 256, 384), ([4100] * 65, 4096, 0, 1024), ([4100] * 65, 4096, 3968, 4096)])
+def test_decode_attention_keys_of_nan_alone_in_their_chunk(lens, prefix, first, end):
+    """NaN keys that a sequence sees make all its outputs NaN, also where a wave, a tile or a chunk has no other key."""
+    gen = generator(len(lens))
+    kc, vc, table, keys, values = paged(gen, lens, 2, 128, 16, prefix)
+    q = fused(gen, len(lens), 8, 2, 128)[0]
+    for p in range(first, end):
+        kc[int(table[0, p // 16]), :, p % 16] = NAN
+    o = w4.decode_attention(q, kc, vc, ints(lens), table, max_len=max(lens), prefix_len=prefix)
+    hit = len(lens) if prefix else 1
+    assert torch.isnan(o[:hit].float()).all()
+    check_decode(o[hit:], q[hit:], keys[hit:], values[hit:], 128 ** -0.5)
+
+
+@pytest.mark.parametrize("lens,prefix,hidden", [([40], 0, 32), ([1100], 0, 128), ([4100] * 65, 4096, 64), ([4100] * 65, 4096, 1100)])
+def test_decode_attention_scores_of_minus_infinity(lens, prefix, hidden):
+    """The first `hidden` keys of sequence 0 or the prefix have scores of -infinity: a weight of 0, however few keys are left."""
+    gen = generator(len(lens) + 1)
+    kc, vc, table, keys, values = paged(gen, lens, 2, 128, 16, prefix)
+    q = fused(gen, len(lens), 8, 2, 128)[0].clone()
+    q[:, :, 0] = q[:, :, 0].abs() + 1
+    for p in range(hidden):
+        kc[int(table[0, p // 16]), :, p % 16, 0] = -INF
+    o = w4.decode_attention(q, kc, vc, ints(lens), table, max_len=max(lens), prefix_len=prefix)
+    check_decode(o, q, [k[hidden:] for k in keys], [v[hidden:] for v in values], 128 ** -0.5)
+
+
+@pytest.mark.parametrize("head", [64, 128])
+@pytest.mark.parametrize("n_q", [4, 512])
+@pytest.mark.parametrize("low", [-60, -87, -95])
+def test_prompt_attention_scores_of_minus_infinity(head, n_q, low):
+    """The first tile's scores are -infinity, the others far below 0: those alone count."""
+    q, k, v = (t.clone() for t in fused(generator(head), 300, n_q, 2, head))
+    q[:, :, 0] = q[:, :, 0].abs() + 1
+    q[:, :, 1], k[:, :, 1] = 8, low * head ** 0.5 / 8
+    k[:64, :, 0] = -INF
+    o = w4.prompt_attention(q, k, v, ints([0, 300]))
+    check_prompt(o[64:], q[64:], k[64:], v[64:], [236], head ** -0.5, heads=[0, 1, n_q - 1])
+
+
 def test_decode_attention_cache_past_32_bits():
     page, n_kv, head = 64, 8, 128
     pages = (5 << 30) // (n_kv * page * head * 2)

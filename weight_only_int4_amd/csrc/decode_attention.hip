@@ -231,7 +231,10 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) {
     const float mw = ml[w * 32 + i];
-    if (mw == -INFINITY && m != -INFINITY) continue;
+    if (mw == -INFINITY && m != -INFINITY) {
+      l += ml[w * 32 + 16 + i];               // 0: nothing seen, or NaN: of nothing but NaN scores
+      continue;
+    }
     const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((mw - m) * c);
     l += f * ml[w * 32 + 16 + i];
 #pragma unroll
@@ -413,7 +416,7 @@ __global__ __launch_bounds__(256) void join_kernel(Kernel k) {
       if (s0 + lane < live) {
         const float2 v = *reinterpret_cast<const float2*>(k.stats + 2 * ((size_t)(s0 + lane) * p.rows + r));
         f = v.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((v.x - m) * c);
-        l += f == 0.0f ? 0.0f : f * v.y;
+        l += f * v.y;                         // v.y without a v.x is 0 (nothing seen) or NaN (scores of NaN alone)
       }
       const int count = min(64, live - s0);
       for (int s1 = 0; s1 < count; s1 += 8 * kAtOnce) {

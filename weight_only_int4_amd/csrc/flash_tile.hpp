@@ -204,16 +204,21 @@ struct Flash {
     if (mine > 0) {
       products(no, yes, 0);
       const int hot = MANY ? min(mine - 1, masked) : mine - 1;
+      bool unset = false;                     // a row without a reference: its scores were all -infinity so far
       auto weigh = [&]() {
         float sum = weights();
-        if (__ballot(!(sum < 0x1p30f))) {
+        if (unset || __ballot(!(sum < 0x1p30f))) {
           asm volatile("");                   // a branch, not both ways and a choice
           raise();
+          unset = __ballot(mref == -INFINITY) != 0;
           sum = weights();
         }
         lsum += sum;
       };
-      if (hot > 0) raise();
+      if (hot > 0) {
+        raise();
+        unset = __ballot(mref == -INFINITY) != 0;
+      }
       // Tiles without masks.  The reference is the first tile's maximum and stays while the p of a row sum to
       // less than 2^30: fp32 and bf16 lose nothing by that, and neither the maximum has to be found nor the
       // accumulators to be scaled.  (Values so large that it overflows come out infinite, and the callers
