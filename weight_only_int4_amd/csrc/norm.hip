@@ -136,11 +136,11 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(const uint16_t* X, c
         }
         uint32_t packed[2];
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const uint32_t lo = __builtin_amdgcn_perm((uint32_t)(int)q[4 * w + 1], (uint32_t)(int)q[4 * w], 0x0C0C0400u);
-          const uint32_t hi = __builtin_amdgcn_perm((uint32_t)(int)q[4 * w + 3], (uint32_t)(int)q[4 * w + 2], 0x04000C0Cu);
-          packed[w] = finite ? lo | hi : 0u;
-          part = __builtin_amdgcn_sdot4((int)packed[w], 0x01010101, part, false);
+        for (int p = 0; p < 2; ++p) {
+          const uint32_t lo = __builtin_amdgcn_perm((uint32_t)(int)q[4 * p + 1], (uint32_t)(int)q[4 * p], 0x0C0C0400u);
+          const uint32_t hi = __builtin_amdgcn_perm((uint32_t)(int)q[4 * p + 3], (uint32_t)(int)q[4 * p + 2], 0x04000C0Cu);
+          packed[p] = finite ? lo | hi : 0u;
+          part = __builtin_amdgcn_sdot4((int)packed[p], 0x01010101, part, false);
         }
         *reinterpret_cast<uint2*>(Xq + row * H + 8 * c) = make_uint2(packed[0], packed[1]);
       }
