@@ -331,7 +331,7 @@ def test_append_past_32_bit_offsets():
 
 # ---------------------------------------------------------------- attention
 
-class Checker:
+class Bounds:
     """Collects one run's elements and holds them to the bounds of this file's head."""
 
     def __init__(self, head):
@@ -365,7 +365,7 @@ class Checker:
 
 def check_prompt(got, q, k, v, lengths, scale, heads=None):
     got, q, k, v = (t.double().cpu() for t in (got, q, k, v))
-    group, c, at = q.shape[1] // k.shape[1], Checker(q.shape[2]), 0
+    group, c, at = q.shape[1] // k.shape[1], Bounds(q.shape[2]), 0
     for n in lengths:
         if n:
             seen = torch.ones(n, n, dtype=torch.bool).tril()
@@ -429,7 +429,7 @@ def test_prompt_attention_many_rows(head, n_q, n_kv, lengths):
     o = w4.prompt_attention(q, k, v, ints(offsets_of(lengths)))
     assert same_bits(o, w4.prompt_attention(q, k, v, ints(offsets_of(lengths))))
     go, gq, gk, gv = (t.double().cpu() for t in (o, q, k, v))
-    c, at, group = Checker(head), 0, n_q // n_kv
+    c, at, group = Bounds(head), 0, n_q // n_kv
     for n in lengths:
         for h in (0, n_q // 2, n_q - 1):
             for first in sorted({0, max(0, n // 2 - 77), max(0, n - 130)}):
@@ -568,7 +568,7 @@ def paged(gen, lens, n_kv, head, page, prefix=0, spare=2, stale=NAN):
 
 def check_decode(got, q, keys, values, scale):
     got, q = got.double().cpu(), q.double().cpu()
-    c = Checker(q.shape[2])
+    c = Bounds(q.shape[2])
     for b in range(len(keys)):
         k, v = keys[b].double().cpu(), values[b].double().cpu()
         if len(k) == 0:
