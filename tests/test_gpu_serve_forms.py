@@ -1,0 +1,71 @@
+"""Single-token attention by form (one launch; narrow chunks; narrow and shared prefix walks): what one form gives
+for seen infinities, NaN and constant values the others give too.  The form of every case is pinned, so that a
+rule that moves it to another one is noticed.  Tolerances as in test_gpu_serve.py."""
+import math
+
+import pytest
+import torch
+
+import weight_only_int4_amd as w4
+from tests import test_gpu_serve as S
+from tests.gpu_util import gpu_available, say
+from tests.serve_plan import plan
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs an MI355X GPU")]
+
+NAN, INF = float("nan"), float("inf")
+
+
+def form_of(lens, n_q, n_kv, head, page, max_len, prefix):
+    return plan(len(lens), n_q, n_kv, head, page, max_len, prefix)
+
+
+# lens, prefix, max_len, the key whose value is not finite, the keys that lie low, form
+LOW = [([280], 0, 280, 40, (32, 64), "direct"),                   # a wave's only tile
+       ([280], 0, 2000, 40, (0, 128), "own"),                     # a chunk
+       ([280], 0, 2000, 40, (32, 64), "own"),                     # a wave's tile of a chunk
+       ([900, 33, 600], 0, 900, 700, (640, 768), "own"),
+       ([270] * 4, 256, 270, 20, (0, 128), "prefix"),
+       ([270] * 4, 256, 270, 264, (256, 270), "prefix"),          # the own tokens under a prefix
+       ([4100] * 65, 4096, 4100, 300, (256, 512), "wide"),
+       ([4100] * 65, 4096, 4100, 4097, (4096, 4100), "wide")]
+
+
+@pytest.mark.parametrize("head", [64, 128])
+@pytest.mark.parametrize("level", [-100.0, -400.0, -INF])
+@pytest.mark.parametrize("lens,prefix,max_len,at,low,form", LOW)
+def test_values_of_keys_that_weigh_nothing(head, level, lens, prefix, max_len, at, low, form):
+    """An infinity or NaN in a value that a sequence sees is not lost where its weight underflows to 0, or is 0 for a
+    score of -infinity: 0 times it is NaN, whichever way the keys are cut.  (A weight that a form keeps above 0 gives
+    the infinity.)  Its other channels are the others' keys alone."""
+    page, n_kv, n_q = 16, 2, 8 if head == 128 else 16
+    say("low", form, head, level, lens[:2], at)
+    assert form_of(lens, n_q, n_kv, head, page, max_len, prefix).form == form
+    for seed, what in enumerate((NAN, INF, -INF)):
+        gen = S.generator(seed)
+        kc, vc, table, keys, values = S.paged(gen, lens, n_kv, head, page, prefix)
+        table = torch.nn.functional.pad(table, (0, max(0, -(-max_len // page) - table.shape[1])), value=-1)
+        q = S.fused(gen, len(lens), n_q, n_kv, head)[0].clone()
+        q[:, :, 0] = 8
+        shared = at < prefix
+        rows = range(len(lens)) if shared else [0]
+        k0 = level * head ** 0.5 / 8
+        for p in range(*low):
+            kc[int(table[0, p // page]), :, p % page, 0] = k0
+        vc[int(table[0, at // page]), :, at % page, 5] = what
+        for b in rows:
+            kept = torch.ones(lens[b], dtype=torch.bool, device="cuda")
+            kept[low[0]:low[1]] = False                            # below the others by 100: they weigh e^-90 at most
+            keys[b], values[b] = keys[b][kept], values[b][kept]
+        o = w4.decode_attention(q, kc, vc, S.ints(lens), table, max_len=max_len, prefix_len=prefix)
+        hit = o[list(rows), :, 5].float()
+        assert torch.isnan(hit).all() if math.isnan(what) else (torch.isnan(hit) | (hit == what)).all()
+        plain, zeroed = o.clone(), [v.clone() for v in values]
+        for b in rows:
+            plain[b, :, 5] = 0
+            zeroed[b][:, :, 5] = 0
+        S.check_decode(plain, q, keys, zeroed, head ** -0.5)
+        if lens[0] <= 300:                                         # the one-launch form of sequence 0 by itself
+            assert form_of(lens[:1], n_q, n_kv, head, page, lens[0], 0).form == "direct"
+            alone = w4.decode_attention(q[:1], kc, vc, S.ints(lens[:1]), table[:1], max_len=lens[0])
+            assert S.same_bits(o[:1], alone)

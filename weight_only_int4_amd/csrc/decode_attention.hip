@@ -24,15 +24,6 @@ typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
 
 constexpr int kWideRows = 128;                // rows of a prefix tile of four waves
 
-struct DecodePlan {
-  int group, prefix;          // queries of a key/value head; keys that the batch shares
-  bool wide, direct;          // prefix rows go 128 to a workgroup (else 16); one chunk in all, no second kernel
-  int p_chunk, p_splits, p_tiles;    // prefix: keys of a chunk, chunks, row tiles
-  int o_chunk, o_splits, o_tiles;    // own tokens
-  int splits;
-  size_t rows, stats_bytes, bytes;   // rows of the batch; workspace: [splits][rows][2], then [splits][rows][head]
-};
-
 // Everything a workgroup needs of a row: where its query lies and how far it sees.
 struct Row {
   int b, hq, limit;
@@ -230,12 +221,8 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
   float l = 0.0f, sum[HEAD / 16] = {};
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) {
-    const float mw = ml[w * 32 + i];
-    if (mw == -INFINITY && m != -INFINITY) {
-      l += ml[w * 32 + 16 + i];               // 0: nothing seen, or NaN: of nothing but NaN scores
-      continue;
-    }
-    const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((mw - m) * c);
+    // (a wave without a reference has the factor 0; it is multiplied like the others, see join_kernel)
+    const float mw = ml[w * 32 + i], f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((mw - m) * c);
     l += f * ml[w * 32 + 16 + i];
 #pragma unroll
     for (int e = 0; e < HEAD / 16; ++e) sum[e] += f * o[(w * 16 + i) * kPad + d + e];
@@ -392,6 +379,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void chunk_kernel(Kernel k) {
 }
 
 // One wave per row: joins its chunks, 16 bytes a lane, so that 64 / (head / 4) chunks are read at once.
+// Chunks of weight 0 are multiplied too: 0 times the infinity or NaN of a value that the row sees is NaN, as in one
+// chunk, and one that it does not see goes when the row is computed once more.
 template <int HEAD>
 __global__ __launch_bounds__(256) void join_kernel(Kernel k) {
   constexpr int kLanes = HEAD / 4, kAtOnce = 64 / kLanes;
@@ -415,8 +404,8 @@ __global__ __launch_bounds__(256) void join_kernel(Kernel k) {
       float f = 0.0f;
       if (s0 + lane < live) {
         const float2 v = *reinterpret_cast<const float2*>(k.stats + 2 * ((size_t)(s0 + lane) * p.rows + r));
-        f = v.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((v.x - m) * c);
-        l += f * v.y;                         // v.y without a v.x is 0 (nothing seen) or NaN (scores of NaN alone)
+        f = __builtin_amdgcn_exp2f((v.x - m) * c);      // without a v.x 0: nothing seen, or scores of NaN or -infinity alone
+        l += f * v.y;
       }
       const int count = min(64, live - s0);
       for (int s1 = 0; s1 < count; s1 += 8 * kAtOnce) {
@@ -430,7 +419,7 @@ __global__ __launch_bounds__(256) void join_kernel(Kernel k) {
         for (int u = 0; u < 8; ++u) {
           const int s = s1 + u * kAtOnce + sub;
           const float fs = __shfl(f, min(s, 63), kWave);
-          if (s < count && fs != 0.0f) o += fs * x[u];       // (a chunk of weight 0 may hold anything)
+          if (s < count) o += fs * x[u];
         }
       }
     }
@@ -454,6 +443,8 @@ __global__ __launch_bounds__(256) void join_kernel(Kernel k) {
 // Chunks are as long as 256 workgroups make them, between 128 keys (four waves' tiles) and 1,024: fewer chunks
 // have less to join (9 sequences of up to 1,214 tokens behind 11,136: 21.1 us, with 512 workgroups 22.2).
 int chunk_of(long long work) { return (int)std::min(1024LL, std::max(128LL, (work / 256 + 127) / 128 * 128)); }
+
+}  // namespace
 
 DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len) {
   DecodePlan p{};
@@ -495,6 +486,8 @@ DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, in
   p.bytes = p.stats_bytes + (size_t)p.splits * p.rows * cache.head * 4;
   return p;
 }
+
+namespace {
 
 long long chunk_blocks(const DecodePlan& p, int B, int n_kv) {
   return (long long)p.p_tiles * p.p_splits * n_kv + (long long)p.o_tiles * p.o_splits * n_kv * B;

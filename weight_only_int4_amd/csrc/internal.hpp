@@ -245,6 +245,16 @@ struct DecodeArgs {
   uint16_t* O;
   void* workspace;
 };
+// A function of its arguments alone, so the size query and the launch agree.
+struct DecodePlan {
+  int group, prefix;          // queries of a key/value head; keys that the batch shares
+  bool wide, direct;          // prefix rows go 128 to a workgroup (else 16); one chunk in all, no second kernel
+  int p_chunk, p_splits, p_tiles;    // prefix: keys of a chunk, chunks, row tiles
+  int o_chunk, o_splits, o_tiles;    // own tokens
+  int splits;
+  size_t rows, stats_bytes, bytes;   // rows of the batch; workspace: [splits][rows][2], then [splits][rows][head]
+};
+DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len);
 bool decode_fits(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len);
 size_t decode_workspace_bytes(int B, int n_q, const w4_kv_cache& cache, int max_len, int prefix_len);
 int launch_decode_attention(const DecodeArgs& g, hipStream_t stream);
