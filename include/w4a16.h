@@ -500,6 +500,7 @@ int mxfp4_a4_gemm(const uint32_t* Xq, const uint8_t* xscales, int M, int K, int 
  *   r multiplies a whole row, so it is left out of the codes and enters the scale: codes
  *   and sums are bit-identical to this definition for every input, and Xq sx is the int8
  *   form of the normed row.  A row with an infinite or NaN v gets codes 0 and sx NaN.
+ *   The mean of squares neither overflows nor underflows, whatever the magnitude of h.
  *   X, residual [T][H] bf16.  weight [H] bf16.  eps >= 0, finite (else W4_ERR_VALUE).
  *   h [T][H] bf16 out, the new residual stream: required with a residual, and may be X or
  *   residual itself; without one it must be NULL.  Y [T][H] bf16 out, may be X.

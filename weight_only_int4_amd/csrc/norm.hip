@@ -26,6 +26,9 @@ __device__ __forceinline__ int row16_sum(int v) {
   return v;
 }
 
+// 2^e, e from -126 to 127
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
 // One workgroup per row of as many waves as CH chunks of 8 channels a thread leave work for (H = 5,120: five
 // waves, two chunks), so that the row is read once, held, and no lane idles.
 template <int CH, bool INT8>
@@ -62,13 +65,58 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(const uint16_t* X, c
       ss = ss + b * b;
     }
   }
-  ss = wave_sum(ss);
-  if ((tid & 63) == 0) red[0][tid >> 6] = ss;
-  __syncthreads();
-  ss = 0.0f;
-  for (int i = 0; i < waves; ++i) ss = ss + red[0][i];
-  const float r = 1.0f / sqrtf(ss / (float)H + eps);
+  auto row_sum = [&](float v) {
+    v = wave_sum(v);
+    if ((tid & 63) == 0) red[0][tid >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int i = 0; i < waves; ++i) v = v + red[0][i];
+    return v;
+  };
+  auto row_max = [&](uint32_t v) {            // of bit patterns of values without a sign: NaN counts as the largest
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, off, kWave));
+    if ((tid & 63) == 0) red[1][tid >> 6] = __uint_as_float(v);
+    __syncthreads();
+    v = 0u;
+    for (int i = 0; i < waves; ++i) v = max(v, __float_as_uint(red[1][i]));
+    return v;
+  };
+  const float mean = row_sum(ss) / (float)H + eps;
+  float r = 1.0f / sqrtf(mean);
+  // Squares overflow from 2^64 on and lose bits below 2^-63 (at most 2^-149 each, which a mean of 2^-100 does not feel).
+  // The sum of such a row is formed again, of its values times 2^-k, k from the largest of them and eps, and r is
+  // then that of the scaled row.  The mean is the same in all threads.  (4,096 x 2,048 in bf16: 12.7 us without the
+  // branch, 13.0 with it, not taken; int8 1 x 2,048: 3.7 and 3.8.)
+  int k = 0;
+  bool scaled = false;
+  if (__builtin_expect(!(mean >= 0x1p-100f && mean < INFINITY), 0)) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t d = reinterpret_cast<const uint32_t*>(&hv[i])[q];
+        top = max(top, max(d << 16 & 0x7FFF0000u, d & 0x7FFF0000u));
+      }
+    top = row_max(top);
+    scaled = top < 0x7F800000u;
+    if (scaled) {
+      k = min(max((int)(__float_as_uint(fmaxf(__uint_as_float(top), sqrtf(eps))) >> 23) - 127, -126), 126);
+      const float down = power_of_two(-k);
+      ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t d = reinterpret_cast<const uint32_t*>(&hv[i])[q];
+          const float a = __uint_as_float(d << 16) * down, b = __uint_as_float(d & 0xFFFF0000u) * down;
+          ss = ss + a * a;
+          ss = ss + b * b;
+        }
+      r = 1.0f / sqrtf(row_sum(ss) / (float)H + eps * down * down);
+    }
+  }
   if constexpr (!INT8) {
+    const float down = power_of_two(-k);      // 1 but for scaled rows
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = tid + i * threads;
@@ -78,15 +126,15 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(const uint16_t* X, c
       uint32_t o[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const bf16x2 y = {(__bf16)((__uint_as_float(d[q] << 16) * r) * __uint_as_float(e[q] << 16)),
-                          (__bf16)((__uint_as_float(d[q] & 0xFFFF0000u) * r) * __uint_as_float(e[q] & 0xFFFF0000u))};
+        const float a = __uint_as_float(d[q] << 16) * down, b = __uint_as_float(d[q] & 0xFFFF0000u) * down;
+        const bf16x2 y = {(__bf16)((a * r) * __uint_as_float(e[q] << 16)),
+                          (__bf16)((b * r) * __uint_as_float(e[q] & 0xFFFF0000u))};
         o[q] = __builtin_bit_cast(uint32_t, y);
       }
       *reinterpret_cast<uint4*>(Y + row * H + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   } else {
-    // max |v| as a maximum of bit patterns: NaN counts as the largest
-    uint32_t top = 0u;
+    uint32_t top = 0u;                        // max |v|
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = tid + i * threads;
@@ -100,19 +148,18 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(const uint16_t* X, c
                            0x7FFFFFFFu);
       }
     }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, kWave));
-    if ((tid & 63) == 0) red[1][tid >> 6] = __uint_as_float(top);
-    __syncthreads();
-    top = 0u;
-    for (int i = 0; i < waves; ++i) top = max(top, __float_as_uint(red[1][i]));
+    top = row_max(top);
     const bool finite = top < 0x7F800000u;
     const float step = __uint_as_float(top) * kStep, t = step > 0.0f ? step : 1.0f;     // (0: of a zero row, or by underflow)
     // Eight divisions a chunk are 75 us at 8,191 x 5,120, eight products 70.  v / t by the reciprocal is off by less than 2^-15 (values to 127, three roundings of 2^-24), so where it lies
     // 2^-14 or more from a half it rounds as the quotient does; the others, and steps so small that the reciprocal
     // might overflow, are divided.
     const float inv = 1.0f / t, far = t >= 0x1p-100f ? 1.0f : 0.0f;
-    if (tid == 0) sx[row] = finite ? t * r : __uint_as_float(0x7FC00000u);
+    if (tid == 0) {
+      // (a scaled row's r 2^-k in two factors: neither leaves the range where t r stays in it)
+      const float product = scaled ? (t * power_of_two(-(k / 2))) * (r * power_of_two(k / 2 - k)) : t * r;
+      sx[row] = finite ? product : __uint_as_float(0x7FC00000u);
+    }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = tid + i * threads;
