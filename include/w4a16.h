@@ -555,7 +555,8 @@ int w4_kv_append(const uint16_t* Q, long long q_stride, const uint16_t* K, long 
  *   O_i = sum_{j <= i} p_ij V_j / sum_{j <= i} p_ij,  p_ij = exp(scale Q_i . K_j - max_j),
  *   over the sequence's own tokens j.  Q [T][n_q][head], K and V [T][n_kv][head], each with
  *   its stride; O [T][n_q][head] bf16 out.  Products of bf16 values summed in fp32, maximum
- *   and sums in fp32, p rounded to bf16 for the product with V, O rounded to nearest even.
+ *   and sums in fp32, p rounded to bf16 (the matrix instruction's operand) and summed as rounded, O rounded to
+ *   nearest even.
  *   scale > 0, finite (else W4_ERR_VALUE).
  *   Size query and workspace as in w4a16_gemv; the size depends only on T, n_q, n_kv, head and B.
  */

@@ -69,3 +69,35 @@ def test_values_of_keys_that_weigh_nothing(head, level, lens, prefix, max_len, a
             assert form_of(lens[:1], n_q, n_kv, head, page, lens[0], 0).form == "direct"
             alone = w4.decode_attention(q[:1], kc, vc, S.ints(lens[:1]), table[:1], max_len=lens[0])
             assert S.same_bits(o[:1], alone)
+
+
+# n_q, n_kv, lens, prefix, form
+CONSTANT = [(4, 2, [300], 0, "direct"), (4, 2, [1200, 900, 0, 1], 0, "own"), (16, 2, [700] * 9, 512, "prefix"), (32, 4, [2100] * 65, 2048, "wide")]
+
+
+@pytest.mark.parametrize("head", [64, 128])
+@pytest.mark.parametrize("n_q,n_kv,lens,prefix,form", CONSTANT)
+def test_constant_values_come_back(head, n_q, n_kv, lens, prefix, form):
+    """Values that are the same in every key are the output, to the bit: the weights are summed as they are multiplied.
+    (Weights of 0.5018 round to 0.5: summed unrounded they would take 0.3% off.)  n additions in fp32 and the joins
+    are off by 2 n 2^-23 <= 2^-10 here, less than the half step (2^-9) that a bf16 value bears."""
+    if head == 64:
+        n_q *= 2
+    assert max(lens) <= 4096 and form_of(lens, n_q, n_kv, head, 16, max(lens), prefix).form == form
+    gen = S.generator(head)
+    kc, vc, table, keys, values = S.paged(gen, lens, n_kv, head, 16, prefix, stale=0)
+    u = torch.randn(n_kv, head, generator=gen, device="cuda").to(S.BF)
+    kc[:, :, :, 0] = -1
+    kc[:, :, ::16, 0] = 0                                          # one key of every tile on top
+    kc[:, :, :, 1:] = 0
+    vc[:] = u[None, :, None]
+    q = torch.zeros(len(lens), n_q, head, dtype=S.BF, device="cuda")
+    q[:, :, 0] = 1
+    o = w4.decode_attention(q, kc, vc, S.ints(lens), table, max_len=max(lens), prefix_len=prefix, scale=-math.log(0.5018))
+    want = u.repeat_interleave(n_q // n_kv, 0)
+    for b, n in enumerate(lens):
+        assert S.same_bits(o[b], want if n else torch.zeros_like(want))
+    if form == "direct":                                           # the prompt's form, whose sums have always been these
+        p = w4.prompt_attention(q.expand(300, n_q, head).contiguous(), kc[0, 0, 0].expand(300, n_kv, head).contiguous(),
+                                u.expand(300, n_kv, head).contiguous(), S.ints([0, 300]))
+        assert S.same_bits(p, want.expand(300, n_q, head))

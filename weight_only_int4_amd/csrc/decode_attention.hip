@@ -184,11 +184,13 @@ __device__ void narrow_chunk(const Kernel& k, const Row& row, bool live, int kvh
       }
       const float mc = mref == -INFINITY ? 0.0f : -mref * c;
       bf16x8 pf;
+      const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r >> 2][r & 3], c, mc));
-        lsum += p;
-        pf[r] = (__bf16)p;
+      for (int r = 0; r < 8; r += 2) {        // the sum is of the rounded p, as the product with V has them
+        const bf16x2 p = {(__bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[r >> 2][r & 3], c, mc)),
+                          (__bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[r >> 2][(r & 3) + 1], c, mc))};
+        lsum = __builtin_amdgcn_fdot2_f32_bf16(p, ones, lsum, false);
+        pf[r] = p[0], pf[r + 1] = p[1];
       }
 #pragma unroll
       for (int db = 0; db < kDb; ++db) {
