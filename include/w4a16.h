@@ -466,7 +466,10 @@ int mxfp4_a4_gemm(const uint32_t* Xq, const uint8_t* xscales, int M, int K, int 
                   const uint8_t* scales, uint16_t* Y, void* workspace, size_t* workspace_bytes, void* stream);
 
 /*
- * Serving operators: what a decoder runs between its quantized linears.  The block is
+ * Serving operators, from what a decoder runs between its quantized linears: the norms, the rotary
+ * append and attention, of whole prompts and of one new token a sequence.  (Not among them: the gated
+ * activation, and attention of several new tokens behind cached ones, which can be appended but
+ * not attended in one call.)  The block is
  * that of w4_block_forward ([AWQ-W4 card] "Base model"; [q326 page] architecture notes);
  * here sequences differ in length, keys and values live in a cache of pages, and the norm
  * can hand int8 activations to w4a8_gemv.  Beside the conventions at the top of this file:
@@ -486,7 +489,9 @@ int mxfp4_a4_gemm(const uint32_t* Xq, const uint8_t* xscales, int M, int K, int 
  *     lengths below 0 as 0; tokens whose page number lies outside [0, pages) or whose
  *     position lies past the table are not written, and attention leaves such keys out.
  *   - Keys and values that a query does not see (later tokens, other sequences, slots past
- *     a sequence's length) may hold anything, NaN and infinities too.
+ *     a sequence's length) may hold anything, NaN and infinities too.  What it sees counts whatever its
+ *     weight: 0 times an infinity or NaN is NaN.  Rows whose result is not finite are computed once more, key
+ *     by key: right, and slow (one NaN in 8,192 tokens of 16 heads of 128: 94 ms where 0.25 are usual).
  *   - A call with no rows (T == 0 or B == 0) succeeds and enqueues nothing.  Outputs must
  *     not overlap inputs or each other, unless said otherwise.
  *
@@ -505,8 +510,8 @@ int mxfp4_a4_gemm(const uint32_t* Xq, const uint8_t* xscales, int M, int K, int 
  *   h [T][H] bf16 out, the new residual stream: required with a residual, and may be X or
  *   residual itself; without one it must be NULL.  Y [T][H] bf16 out, may be X.
  *   Xq [T][H] int8, sx [T] fp32, xsum [T][H/128] int32 out: w4a8_gemv reads any 16 rows of
- *   them.  H a positive multiple of 8 (w4_rmsnorm) or 128 (w4a8_rmsnorm), at most 65,536
- *   (else W4_ERR_SHAPE).
+ *   them.  H a positive multiple of 8 (w4_rmsnorm) or 128 (w4a8_rmsnorm), at most 65,536; T at most
+ *   4,194,303 (else W4_ERR_SHAPE).
  */
 int w4_rmsnorm(const uint16_t* X, const uint16_t* residual, int T, int H, const uint16_t* weight, float eps,
                uint16_t* h, uint16_t* Y, void* stream);

@@ -1,6 +1,8 @@
 // Attention of one query by one wave, key by key: slow, and exact about what is not seen.  The
 // attention kernels come back to it for rows whose result is not finite: there a matrix product may have
-// multiplied a weight of 0 with an infinity or NaN in a value that the row does not see.
+// multiplied a weight of 0 with an infinity or NaN in a value that the row does not see.  Rows that see one come here
+// too.  A row of 64 keys takes 23 us, and a wave's rows go one after another: one NaN among 8,192 tokens of 16 heads of
+// 128 makes a call of 0.25 ms one of 94, a decode step of 64 sequences of 2,000 tokens one of 1.0 where it takes 0.1.
 #pragma once
 
 #include <math.h>

@@ -2,13 +2,14 @@
 //
 // The keys are split: the prefix into chunks that all sequences' queries of a key/value head see together
 // (as many rows as the batch has sequences times the group), each sequence's own tokens into chunks of their
-// own.  Every chunk gives, per row, the largest score m, the sum l of p = exp(scale (s - m)) and sum p V in
-// fp32; a second kernel joins a row's chunks: O = sum_c w_c O_c / sum_c w_c l_c, w_c = exp(scale (m_c - max m)).
+// own.  Every chunk gives, per row, a reference m, the sum l of p = exp(scale (s - m)) and sum p V in fp32; a
+// second kernel joins a row's chunks: O = sum_c w_c O_c / sum_c w_c l_c, w_c = exp(scale (m_c - max m)).  (m is no
+// more than the largest score, and less by as much as p may grow: to 2^8 in 16 rows' chunks, to sums of 2^30 in 128 rows'.)
 // Chunk sizes follow from what the host knows, so a captured graph serves any lengths.
 //
 // What bounds it: long lengths the memory (64 sequences of 2,000 tokens behind 8,192, 32 heads on 8: 302 MB from
-// it and 66 us in the chunks, 4.6 TB/s); short ones the way of one chunk from the lengths over the table, keys,
-// scores and values to LDS and out, 5 us, and a second launch of 4 (16 sequences of 512 behind 2,048: 9.6 and 4.5).
+// it and 64 us in the chunks, 4.7 TB/s); short ones the way of one chunk from the lengths over the table, keys,
+// scores and values to LDS and out, 5 us, and a second launch of 4 (16 sequences of 512 behind 2,048: 9.5 and 4.4).
 #include "attend.hpp"
 #include "flash_tile.hpp"
 
@@ -350,7 +351,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void chunk_kernel(Kernel k) {
   int id = blockIdx.x;
   const int per_tile = g.cache.n_kv * p.p_splits;
   if (id < per_tile * p.p_tiles) {
-    // prefix: row tile, chunk, key/value head (one chunk's row tiles on one XCD, 8 apart)
+    // prefix: row tile, chunk, key/value head (where the chunks of all heads are a multiple of 8, one chunk's row
+    // tiles are on one XCD)
     const int tile = id / per_tile;
     id -= tile * per_tile;
     const int split = id / g.cache.n_kv, kvh = id - split * g.cache.n_kv;
@@ -472,8 +474,11 @@ DecodePlan plan_decode(int B, int n_q, const w4_kv_cache& cache, int max_len, in
     p.p_tiles = (int)(p.wide ? (rows + kWideRows - 1) / kWideRows : (rows + 15) / 16);
     const long long p_work = (long long)p.prefix * p.p_tiles * cache.n_kv;
     // wide: a workgroup per CU, or longer walks on fewer of them while the own tokens are many enough to be read
-    // beside them (64 sequences of 2,000 tokens behind 8,192: 70.5 us, with a workgroup per CU 78.8; of 1,000: 50.2
-    // and 56.7; twice or half the divisor changes nothing)
+    // beside them (a workgroup per CU, and this; 8 key/value heads of 128, group 4: 64 sequences of up to 2,000 tokens
+    // behind 8,192 71.6 and 64.4 us, of 1,000 51.2 and 47.4, 128 of 1,000 behind 4,096 75.0 and 66.8, 200 of 700 behind
+    // 2,048 81.5 and 74.4, 100 of 500 behind 8,192 47.0 and 47.4, 48 of 3,000 behind 12,288 79.5 and 80.0; heads of 64
+    // 40.7 and 39.3; but 2 heads, group 8, 128 of 1,500 behind 6,144 39.9 and 43.5; twice or half the divisor changes
+    // nothing)
     const long long along = (long long)std::min(1024.0, (double)o_work / p.o_tiles * cache.head / 45000);
     p.p_chunk = p.wide ? (int)std::min(1024LL, std::max(256LL, (std::max(p_work / 256, along) + 63) / 64 * 64))
                        : chunk_of(p_work + o_work);

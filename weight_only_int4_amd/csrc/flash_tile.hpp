@@ -9,9 +9,11 @@
 //
 // What bounds it: per tile and wave 32 matrix instructions of 32 cycles (head 128; 16 for head 64) and
 // about 100 vector instructions of 4, of which 32 exp2 take 8, and every matrix instruction holds the vector
-// ALU up for about 9; on random data the chip also lowers its clock (1 x 8192 tokens of 16 heads of 128: 251 us,
-// 1.1 PFLOP/s of the 1.42 that a large matrix product reaches; on zeros 204.  12 x 2047 ragged at head 64: 96).
-// Two waves a SIMD overlap the one with the other.  Measured and not kept: the weights of tile t + 1 woven between
+// ALU up for about 9; on random data the chip also lowers its clock (1 x 8192 tokens of 16 heads of 128: 249 us,
+// 1.1 PFLOP/s of the 1.41 that a large matrix product reaches; on zeros 204).  Two waves a SIMD overlap the one with
+// the other.  That is a long walk's; a short one is bound by what comes before and after its tiles, about 9 us of a
+// workgroup at head 64 (12 x 2047 ragged, 32 heads: 96 us, of which the tiles would take 61).
+// Measured and not kept: the weights of tile t + 1 woven between
 // the matrix instructions of tile t in one wave (no change at head 128, where another 50 registers are no loss;
 // 97 -> 119 us at head 64, where they cost waves), the two waves of a SIMD in opposite phases by a second barrier
 // or by s_setprio (no change), 64 queries a wave with all 512 registers (1 x 8192: 395 us), tiles of 128 keys at

@@ -8,7 +8,7 @@
 //
 // What bounds it: a few rows the launch (int8, 1 x 2,048: 3.1 us in the kernel, a round trip to memory and two
 // barriers); many rows the memory (int8, 8,191 x 5,120 with a residual: 294 MB in 65 to 70 us, 4.5 to 4.2 TB/s; 4,096 x
-// 2,048 in bf16: 67 MB in 11.5 to 12.1 us, part of it from the caches).
+// 2,048 in bf16: 67 MB in 11.6 to 12.2 us, part of it from the caches).
 #include "serve.hpp"
 
 #pragma clang fp contract(off)
@@ -151,9 +151,9 @@ __global__ __launch_bounds__(kMostThreads) void norm_kernel(const uint16_t* X, c
     top = row_max(top);
     const bool finite = top < 0x7F800000u;
     const float step = __uint_as_float(top) * kStep, t = step > 0.0f ? step : 1.0f;     // (0: of a zero row, or by underflow)
-    // Eight divisions a chunk are 75 us at 8,191 x 5,120, eight products 70.  v / t by the reciprocal is off by less than 2^-15 (values to 127, three roundings of 2^-24), so where it lies
-    // 2^-14 or more from a half it rounds as the quotient does; the others, and steps so small that the reciprocal
-    // might overflow, are divided.
+    // Eight divisions a chunk are 75 us at 8,191 x 5,120, eight products 70.  v / t by the reciprocal is off by less
+    // than 2^-15 (values to 127, three roundings of 2^-24), so where it lies 2^-14 or more from a half it rounds as the
+    // quotient does; the others, and steps so small that the reciprocal might overflow, are divided.
     const float inv = 1.0f / t, far = t >= 0x1p-100f ? 1.0f : 0.0f;
     if (tid == 0) {
       // (a scaled row's r 2^-k in two factors: neither leaves the range where t r stays in it)

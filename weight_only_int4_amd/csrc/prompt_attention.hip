@@ -214,7 +214,8 @@ bool prompt_fits(int T, int n_q, int n_kv, int B) {
 
 int launch_prompt_attention(const PromptArgs& g, hipStream_t st) {
   // eight waves share each key tile, four end sooner where there are few workgroups (8 x 512 tokens of 16
-  // heads: 24.3 us with eight, 21.1 with four; 1 x 8192: 239 and 252)
+  // heads: 24.3 us with eight, 21.1 with four; 1 x 8192: 239 and 252).  The rule looks at the rows alone: many
+  // sequences shorter than 256 tokens by the heads of a group leave waves of the eight without queries.
   const bool wide = (long long)g.T * g.n_q >= 512 * 256;
   if (g.head == 64) return wide ? launch<64, 8>(g, st) : launch<64, 4>(g, st);
   return wide ? launch<128, 8>(g, st) : launch<128, 4>(g, st);
